@@ -83,6 +83,12 @@ typedef struct CUstream_st* moe_stream_t; /* same object as cudaStream_t */
 #define MOE_OUT_F32  0 /* fp32 (default): the residual stream's dtype */
 #define MOE_OUT_BF16 1
 
+/* dtypes of the norms' and the 8-bit operators' tensors */
+#define MOE_DT_F32  0
+#define MOE_DT_BF16 1
+#define MOE_DT_F16  2
+#define MOE_DT_E4M3 3 /* 8 bits, with a scale for each 128 columns; where a parameter says so */
+
 /* dtype of w_down / shared_down (bf16 weight format only) */
 #define MOE_DOWN_BF16 0 /* as given; each tile is converted to fp16 in shared memory */
 #define MOE_DOWN_F16  1 /* prepared once with moe_convert_bf16_to_f16 (load time) */
@@ -419,7 +425,12 @@ MOE_API int moe_wait_selftest(void* err_ws, uint64_t limit_ns, moe_stream_t stre
 #define MOE_K_ROUTE_STATS   14  /* router telemetry: the final sum over blocks (moe_route_stats) */
 #define MOE_K_BWD_GEMM      15  /* backward tcgen05 GEMMs (moe_expert_ffn_backward) */
 #define MOE_K_BWD_SMALL     16  /* backward schedule, gathers, zeroing, reductions */
-#define MOE_K_COUNT         17
+#define MOE_K_NORM          17  /* norms before and after a block (moe_norm_forward, moe_norm_residual_forward) */
+#define MOE_K_NORM_BWD      18  /* their gradients: the rows, then the sums over tokens */
+#define MOE_K_QUANT_F8      19  /* rows or weights to e4m3 (moe_quantize_f8, moe_quantize_f8_weights) */
+#define MOE_K_TC_F8         20  /* 8-bit products on the tcgen05 tiles (moe_matmul_f8, moe_gated_f8) */
+#define MOE_K_STREAM_F8     21  /* the same for a few rows, streaming the weights */
+#define MOE_K_COUNT         22
 
 /*
  * Gradients written by moe_expert_ffn_backward (device pointers, fp32, row-major).
@@ -472,6 +483,187 @@ MOE_API int moe_expert_ffn_backward(const moe_params* p, const uint16_t* x, cons
               const float* topk_w, const int32_t* offsets, const int32_t* sorted_token,
               const int32_t* sorted_pair, const int32_t* pair_row, const moe_weights* w,
               const float* dout, const moe_grads* g, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ norms around a block
+ *
+ * The layer's block takes a normed copy of the residual stream and its result
+ * goes back into the stream. (The pages show the layer's two ends only:
+ * "mini-AGI PR #4" run() returns its result in the residual stream's dtype.)
+ *   before:  y = N(x)
+ *   after:   out = alpha * r + beta * gate * N(y)
+ *            x_next = N2(out), the next block's norm, from out as it is stored
+ *   N(x) = xhat * (w + weight_offset) + b
+ *   MOE_NORM_RMS:   xhat = x / sqrt(mean(x^2) + eps)
+ *   MOE_NORM_LAYER: xhat = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps)
+ *   MOE_NORM_NONE:  N(x) = x, without weights (after the block only)
+ * A NULL weight is 1 (weight_offset then has no part), a NULL bias 0.
+ * Sums and statistics are fp32; each output is rounded once to its dtype.
+ * Rows are [T, d] with their elements next to each other and ld_* elements from
+ * row to row; any d up to MOE_NORM_MAX_D, any stride and any element-aligned
+ * pointer is taken. Rows of a multiple of 8 elements that all start on 16 bytes
+ * (every tensor of the call) are read in 16-byte vectors; others element by element.
+ * T = 0: nothing is launched; gradients summed over tokens are set to zero.
+ */
+#define MOE_NORM_NONE  0
+#define MOE_NORM_RMS   1
+#define MOE_NORM_LAYER 2
+#define MOE_NORM_MAX_D 8192 /* larger d: MOE_ERR_UNSUPPORTED */
+
+#define MOE_GATE_NONE    0
+#define MOE_GATE_CHANNEL 1 /* gate [d]: one value a channel, for every token */
+#define MOE_GATE_TOKEN   2 /* gate [T]: one value a token, for every channel */
+
+typedef struct moe_norm_params {
+    int32_t T;
+    int32_t d;
+    int32_t kind;          /* MOE_NORM_* of the call's norm */
+    int32_t next_kind;     /* moe_norm_residual_forward: N2; MOE_NORM_NONE: no x_next. Else MOE_NORM_NONE */
+    float eps;             /* >= 0; both norms */
+    float weight_offset;   /* added to every weight (1 for weights stored around zero); both norms */
+    int32_t stream_dtype;  /* MOE_DT_F32 | BF16 | F16: the residual stream (x, r, out, dx, dr, dout) */
+    int32_t block_dtype;   /* the block's rows (y of both ends, x_next, dy) */
+    int32_t param_dtype;   /* weights, biases and gates */
+    int32_t gate_kind;     /* MOE_GATE_* (after the block; else MOE_GATE_NONE) */
+    float alpha;           /* residual scale */
+    float beta;            /* branch scale */
+    int64_t ld_stream;     /* elements from row to row of stream tensors; 0: d */
+    int64_t ld_block;      /* the same for block tensors */
+} moe_norm_params;
+
+/* Gradients summed over tokens, fp32, each NULL if not wanted. */
+typedef struct moe_norm_grads {
+    float* dweight;  /* [d]; needs a weight */
+    float* dbias;    /* [d] */
+    float* dgate;    /* [d] (per channel) or [T] (per token); after the block only */
+} moe_norm_grads;
+
+/* Bytes of workspace of the two backward calls; 0 on invalid params. */
+MOE_API size_t moe_norm_workspace_size(const moe_norm_params* p);
+
+/*
+ * moe_norm_forward — y = N(x): the norm before a block.
+ * x      [T, d] stream_dtype
+ * y      [T, d] block_dtype, or NULL when q8 is given; may be x itself (same dtype and stride)
+ * q8, s8 NULL, or N(x) (before its rounding to block_dtype) as moe_quantize_f8 gives it:
+ *        e4m3 [T, d] (row stride d) and its scales fp32 [ceil(d/128), T]. Needs d a multiple of 16
+ *        and every tensor's rows on 16 bytes (MOE_ERR_INVALID_ARG / MOE_ERR_MISALIGNED)
+ * mean, rstd  fp32 [T] for the backward call, or NULL (mean is 0 for RMS)
+ */
+MOE_API int moe_norm_forward(const moe_norm_params* p, const void* x, const void* weight, const void* bias, void* y,
+              uint8_t* q8, float* s8, float* mean, float* rstd, moe_stream_t stream);
+
+/*
+ * moe_norm_backward — gradients of moe_norm_forward for an upstream dy.
+ * With G = dy (w + weight_offset): dx = dres + rstd (G - mean(G) - xhat mean(G xhat)) (RMS without
+ * mean(G)); dweight = sum_t dy xhat; dbias = sum_t dy.
+ * dres  [T, d] stream_dtype: the gradient that reaches x past the block, added to dx; or NULL
+ * mean, rstd  as the forward call wrote them (mean may be NULL for RMS)
+ * dx    [T, d] stream_dtype; may be dres itself
+ * ws    moe_norm_workspace_size bytes (NULL without dweight and dbias). Deterministic.
+ */
+MOE_API int moe_norm_backward(const moe_norm_params* p, const void* x, const void* weight, const void* dy,
+              const void* dres, const float* mean, const float* rstd, void* dx, const moe_norm_grads* g, void* ws,
+              size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_norm_residual_forward — out = alpha r + beta gate N(y), and the next block's norm of out in
+ * the same pass over the row.
+ * resid  [T, d] stream_dtype; out [T, d] stream_dtype, may be resid itself
+ * y      [T, d] block_dtype: the block's result
+ * gate   param_dtype [d] or [T] by gate_kind; NULL for MOE_GATE_NONE
+ * x_next [T, d] block_dtype, q8, s8: N2(out), as y, q8, s8 of moe_norm_forward; NULL without a next norm
+ * mean, rstd, next_mean, next_rstd  fp32 [T] or NULL
+ */
+MOE_API int moe_norm_residual_forward(const moe_norm_params* p, const void* resid, const void* y, const void* weight,
+              const void* bias, const void* gate, void* out, float* mean, float* rstd, const void* next_weight,
+              const void* next_bias, void* x_next, uint8_t* q8, float* s8, float* next_mean, float* next_rstd,
+              moe_stream_t stream);
+
+/*
+ * moe_norm_residual_backward — gradients of out = alpha r + beta gate N(y) for an upstream dout
+ * (with a next norm, dout is the dx that moe_norm_backward of that norm gives from the stream's
+ * gradient as its dres; next_kind has no part here).
+ * dresid [T, d] stream_dtype = alpha dout, or NULL (it may be dout itself)
+ * dy     [T, d] block_dtype: through N, with D = beta gate dout as N's upstream gradient
+ * dweight = sum_t D xhat, dbias = sum_t D (needs a bias), dgate = beta sum dout N(y) over tokens or channels
+ * bias   is needed for a gate's gradient where the forward had one
+ * ws     moe_norm_workspace_size bytes (NULL without dweight, dbias and a channel gate's dgate). Deterministic.
+ */
+MOE_API int moe_norm_residual_backward(const moe_norm_params* p, const void* y, const void* weight, const void* bias,
+              const void* gate, const void* dout, const float* mean, const float* rstd, void* dresid, void* dy,
+              const moe_norm_grads* g, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ products in 8-bit floating point
+ *
+ * Values in e4m3 (4 exponent bits, 3 fraction bits, largest 448, no infinities) with an fp32 scale
+ * for each block of 128: of a row's columns (activations), or of 128 x 128 (weights).
+ *   rows     q [rows, K] bytes; scales [ceil(K/128), rows]: x[r, c] = q[r, c] * s[c / 128, r]
+ *   weights  q [E, N, K] bytes, K-major; scales [E, ceil(N/128), ceil(K/128)]
+ *   s = max(amax / 448, 2^-126), q = e4m3(x / s), nearest even; an infinity or a NaN makes its
+ *   whole block read back as NaN.
+ * K is a multiple of 16, N of 8; the last block of either may be partial. Byte tensors lie on 16
+ * bytes (MOE_ERR_MISALIGNED). Rows by expert are as moe_permute leaves them: expert e has rows
+ * [offsets[e], offsets[e+1]); rows from offsets[E] on are neither read nor written.
+ */
+
+/*
+ * moe_quantize_f8 — rows to e4m3, optionally gathered.
+ * x         x_dtype (MOE_DT_F32 | BF16 | F16) [src_rows, K], ld_x elements from row to row (0: K)
+ * row_index int32 [rows]: row r of q is x[row_index[r]] (sorted_token of moe_permute); NULL: x[r].
+ *           Out-of-range entries set MOE_DEVERR_BOUNDS, and their rows are left as they were
+ * n_rows    device int32 (offsets + E of moe_permute): rows from *n_rows on are left; NULL: all
+ * q, s      [rows, K] bytes and [ceil(K/128), rows]
+ * ws        256 bytes: the error word
+ */
+MOE_API int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int64_t ld_x, int64_t src_rows,
+              const int32_t* row_index, const int32_t* n_rows, uint8_t* q, float* s, void* ws, size_t ws_bytes,
+              moe_stream_t stream);
+
+/*
+ * moe_quantize_f8_weights — weights to e4m3, done once at load time.
+ * w  w_dtype [E, N, K], or [E, K, N] with transposed = 1 (as the bf16 layer has them: [E, d, f] and
+ *    [E, f, d]); rows next to each other. q [E, N, K], s [E, ceil(N/128), ceil(K/128)].
+ */
+MOE_API int moe_quantize_f8_weights(int32_t E, int32_t N, int32_t K, const void* w, int32_t w_dtype,
+              int32_t transposed, uint8_t* q, float* s, moe_stream_t stream);
+
+typedef struct moe_f8_params {
+    int64_t rows;        /* rows of the buffers, < 2^31; 0: nothing is launched */
+    int32_t K;           /* reduction length */
+    int32_t N;           /* columns of the result (of each of the two projections) */
+    int32_t E;           /* 1..256; 1 without offsets: one dense product */
+    int32_t out_dtype;   /* MOE_DT_F32 | BF16 | F16; moe_gated_f8 also MOE_DT_E4M3 (N a multiple of 16) */
+    float swiglu_limit;  /* moe_gated_f8: as in moe_params */
+    int32_t variant;     /* MOE_VARIANT_AUTO, or _TENSOR / _STREAM to force one kind of kernel */
+} moe_f8_params;
+
+/* Bytes of workspace of moe_matmul_f8 and moe_gated_f8 (the error word); 0 on invalid params. */
+MOE_API size_t moe_f8_workspace_size(const moe_f8_params* p);
+
+/*
+ * moe_matmul_f8 — out[r, n] = w_r * sum_k a[r, k] b[e, n, k], e the expert of row r.
+ * Products of e4m3 values on the tensor cores; each 128-block's sum is multiplied by its two scales
+ * and added in fp32.
+ * a, a_scale  [rows, K] bytes, [ceil(K/128), rows]; b, b_scale: weights as above
+ * offsets     int32 [E+1], or NULL with E = 1 (every row)
+ * sorted_pair, topk_w  w_r = topk_w[sorted_pair[r]] (1 where sorted_pair[r] < 0), as moe_expert_ffn
+ *             weighs its rows for moe_combine (out_dtype MOE_DT_F16); both NULL: 1
+ * out         [rows, N] out_dtype; MOE_DT_F16 values beyond +-65504 set MOE_DEVERR_RANGE
+ */
+MOE_API int moe_matmul_f8(const moe_f8_params* p, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+              const uint8_t* b, const float* b_scale, const int32_t* sorted_pair, const float* topk_w, void* out,
+              void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/*
+ * moe_gated_f8 — h = silu(clamp(g, -L, L)) * clamp(u, -L, L) with g = a W_gate^T, u = a W_up^T (as
+ * moe_matmul_f8, in fp32), both projections, the activation and the product in one kernel.
+ * w_gate, s_gate, w_up, s_up  weights [E, N, K] and their scales
+ * h        [rows, N] out_dtype. MOE_DT_E4M3: rounded as moe_quantize_f8 does, ready for
+ *          moe_matmul_f8, with h_scale fp32 [ceil(N/128), rows] (else h_scale NULL)
+ */
+MOE_API int moe_gated_f8(const moe_f8_params* p, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+              const uint8_t* w_gate, const float* s_gate, const uint8_t* w_up, const float* s_up, void* h,
+              float* h_scale, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
  * Number of kernel launches one call of `which` (MOE_WS_ROUTE .. MOE_WS_BACKWARD,

@@ -28,6 +28,10 @@ DOWN_BF16, DOWN_F16 = 0, 1
 WEIGHTS_BF16, WEIGHTS_Q4G32 = 0, 1
 VARIANT_AUTO, VARIANT_TENSOR, VARIANT_STREAM = 0, 1, 2
 TILE_AUTO, TILE_ONE, TILE_PAIR = 0, 1, 2
+DT_F32, DT_BF16, DT_F16, DT_E4M3 = range(4)
+NORM_NONE, NORM_RMS, NORM_LAYER = range(3)
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = range(3)
+NORM_MAX_D = 8192  # MOE_NORM_MAX_D
 WS_ROUTE, WS_PERMUTE, WS_EXPERT_FFN, WS_COMBINE, WS_FORWARD, WS_FORWARD_HOST, WS_ROUTE_STATS, WS_BACKWARD = range(8)
 
 # every entry point declared in include/moe.h
@@ -36,13 +40,16 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_capacity", "moe_max_rows", "
            "moe_get_error", "moe_clear_error", "moe_set_wait_limit_ns", "moe_launch_count",
            "moe_profile_enable", "moe_profile_collect", "moe_convert_bf16_to_f16",
            "moe_permute_noalloc", "moe_forward_host_async", "moe_wait_selftest", "moe_tile_ctas",
-           "moe_route_stats", "moe_expert_ffn_backward", "moe_variant_table")
+           "moe_route_stats", "moe_expert_ffn_backward", "moe_variant_table",
+           "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward", "moe_norm_residual_forward",
+           "moe_norm_residual_backward", "moe_quantize_f8", "moe_quantize_f8_weights", "moe_f8_workspace_size",
+           "moe_matmul_f8", "moe_gated_f8")
 NOALLOC_MAX_PAIRS = 262144  # MOE_NOALLOC_MAX_PAIRS
 
 # kernel ids (MOE_K_*), in order
 KERNELS = ("route", "perm_count", "perm_scan", "perm_scatter", "schedule", "gather", "tc_gateup", "tc_down",
            "stream_gateup", "stream_reduce", "stream_down", "combine", "convert", "front", "route_stats",
-           "bwd_gemm", "bwd_small")
+           "bwd_gemm", "bwd_small", "norm", "norm_bwd", "quant_f8", "tc_f8", "stream_f8")
 
 
 class MoeError(RuntimeError):
@@ -66,6 +73,23 @@ class Weights(ctypes.Structure):
 class Grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "dw_gate", "dw_up", "dw_down", "d_topk_w", "dlogits",
                                                "dshared_gate", "dshared_up", "dshared_down")]
+
+
+class NormParams(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32), ("next_kind", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("stream_dtype", ctypes.c_int32),
+                ("block_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("ld_stream", ctypes.c_int64),
+                ("ld_block", ctypes.c_int64)]
+
+
+class NormGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dweight", "dbias", "dgate")]
+
+
+class F8Params(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("E", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("swiglu_limit", ctypes.c_float), ("variant", ctypes.c_int32)]
 
 
 _lib = None
@@ -107,6 +131,20 @@ def lib() -> ctypes.CDLL:
             "moe_expert_ffn_backward": ([_P, _V, _V, _V, _V, _V, _V, _V, ctypes.POINTER(Weights), _V,
                                          ctypes.POINTER(Grads), _V, _S, _V], ctypes.c_int),
         }
+        i32, i64 = ctypes.c_int32, ctypes.c_int64
+        N, G, F = ctypes.POINTER(NormParams), ctypes.POINTER(NormGrads), ctypes.POINTER(F8Params)
+        sig.update({
+            "moe_norm_workspace_size": ([N], _S),
+            "moe_norm_forward": ([N] + [_V] * 9, ctypes.c_int),
+            "moe_norm_backward": ([N] + [_V] * 7 + [G, _V, _S, _V], ctypes.c_int),
+            "moe_norm_residual_forward": ([N] + [_V] * 16, ctypes.c_int),
+            "moe_norm_residual_backward": ([N] + [_V] * 9 + [G, _V, _S, _V], ctypes.c_int),
+            "moe_quantize_f8": ([i64, i32, _V, i32, i64, i64, _V, _V, _V, _V, _V, _S, _V], ctypes.c_int),
+            "moe_quantize_f8_weights": ([i32, i32, i32, _V, i32, i32, _V, _V, _V], ctypes.c_int),
+            "moe_f8_workspace_size": ([F], _S),
+            "moe_matmul_f8": ([F] + [_V] * 9 + [_S, _V], ctypes.c_int),
+            "moe_gated_f8": ([F] + [_V] * 10 + [_S, _V], ctypes.c_int),
+        })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
@@ -321,3 +359,220 @@ def prepare_down_f16(w_down, stream=None):
     out = torch.empty(w_down.shape, dtype=torch.float16, device=w_down.device)
     convert_bf16_to_f16(w_down, out, stream=stream)
     return out
+
+
+# ------------------------------------------------------------------ norms around a block
+
+def _dt(t) -> int:
+    """The library's dtype code of a tensor."""
+    import torch
+    codes = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+    if t.dtype not in codes:
+        raise MoeError(f"unsupported dtype {t.dtype}")
+    return codes[t.dtype]
+
+
+def _fits(what, stream, *specs):
+    """Checks tensors against (name, tensor, shape, dtypes): on the device the call runs on, of the
+    shape and one of the dtypes, and contiguous where the shape is followed by True. None passes."""
+    import torch
+    dev = stream.device if stream is not None else torch.device("cuda", torch.cuda.current_device())
+    if dev.index != torch.cuda.current_device():
+        raise MoeError(f"{what}: the stream is not on the current device")
+    for name, t, shape, dtypes, dense in specs:
+        if t is None:
+            continue
+        if t.device != dev:
+            raise MoeError(f"{what}: {name} is on {t.device}, the call runs on {dev}")
+        if tuple(t.shape) != tuple(shape):
+            raise MoeError(f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+        if t.dtype not in dtypes:
+            raise MoeError(f"{what}: {name} is {t.dtype}")
+        if dense and not t.is_contiguous():
+            raise MoeError(f"{what}: {name} is not contiguous")
+
+
+def _dtypes(code):
+    import torch
+    return ((torch.float32,), (torch.bfloat16,), (torch.float16,), (torch.float8_e4m3fn, torch.uint8))[code]
+
+
+def norm_params(T, d, kind=NORM_RMS, next_kind=NORM_NONE, eps=1e-6, weight_offset=0.0, stream_dtype=DT_F32,
+                block_dtype=DT_BF16, param_dtype=DT_F32, gate_kind=GATE_NONE, alpha=1.0, beta=1.0, ld_stream=0,
+                ld_block=0) -> NormParams:
+    return NormParams(T, d, kind, next_kind, eps, weight_offset, stream_dtype, block_dtype, param_dtype, gate_kind,
+                      alpha, beta, ld_stream, ld_block)
+
+
+def norm_workspace(p: NormParams, device="cuda"):
+    """A device workspace of the size the norms' backward calls need (256-byte aligned)."""
+    import torch
+    n = int(lib().moe_norm_workspace_size(ctypes.byref(p)))
+    if n == 0:
+        raise MoeError("invalid parameters")
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+def _norm_grads(dw, db, dgate) -> NormGrads:
+    return NormGrads(*(None if t is None else t.data_ptr() for t in (dw, db, dgate)))
+
+
+def _rows_ok(what, p, ld, **tensors):
+    """Row tensors: elements next to each other and the params' stride from row to row."""
+    for name, t in tensors.items():
+        if t is not None and t.shape[0] > 0 and (t.stride(1) != 1 and t.shape[1] > 1 or
+                                                 t.shape[0] > 1 and t.stride(0) != (ld or p.d)):
+            raise MoeError(f"{what}: {name} has strides {t.stride()}, the params say {(ld or p.d, 1)}")
+
+
+def norm_forward(p: NormParams, x, y, weight=None, bias=None, q8=None, s8=None, mean=None, rstd=None, stream=None):
+    """moe_norm_forward: y = N(x), the norm before a block; q8, s8: N(x) in e4m3 with its scales."""
+    f32, par = _dtypes(DT_F32), _dtypes(p.param_dtype)
+    row = (p.T, p.d)
+    _fits("moe_norm_forward", stream, ("x", x, row, _dtypes(p.stream_dtype), False),
+          ("y", y, row, _dtypes(p.block_dtype), False), ("weight", weight, (p.d,), par, True),
+          ("bias", bias, (p.d,), par, True), ("q8", q8, row, _dtypes(DT_E4M3), True),
+          ("s8", s8, ((p.d + 127) // 128, p.T), f32, True), ("mean", mean, (p.T,), f32, True),
+          ("rstd", rstd, (p.T,), f32, True))
+    _rows_ok("moe_norm_forward", p, p.ld_stream, x=x)
+    _rows_ok("moe_norm_forward", p, p.ld_block, y=y)
+    check(lib().moe_norm_forward(ctypes.byref(p), _p(x), _p(weight), _p(bias), _p(y), _p(q8), _p(s8), _p(mean),
+                                 _p(rstd), _stream(stream)), "moe_norm_forward")
+
+
+def norm_backward(p: NormParams, x, dy, mean, rstd, dx, ws=None, weight=None, dres=None, dw=None, db=None,
+                  stream=None):
+    """moe_norm_backward: gradients of norm_forward; dres is added to dx. ws: norm_workspace(p)."""
+    f32, par = _dtypes(DT_F32), _dtypes(p.param_dtype)
+    row, st = (p.T, p.d), _dtypes(p.stream_dtype)
+    _fits("moe_norm_backward", stream, ("x", x, row, st, False), ("dy", dy, row, _dtypes(p.block_dtype), False),
+          ("dres", dres, row, st, False), ("dx", dx, row, st, False), ("weight", weight, (p.d,), par, True),
+          ("mean", mean, (p.T,), f32, True), ("rstd", rstd, (p.T,), f32, True), ("dw", dw, (p.d,), f32, True),
+          ("db", db, (p.d,), f32, True))
+    _rows_ok("moe_norm_backward", p, p.ld_stream, x=x, dres=dres, dx=dx)
+    _rows_ok("moe_norm_backward", p, p.ld_block, dy=dy)
+    check(lib().moe_norm_backward(ctypes.byref(p), _p(x), _p(weight), _p(dy), _p(dres), _p(mean), _p(rstd), _p(dx),
+                                  ctypes.byref(_norm_grads(dw, db, None)), _p(ws), 0 if ws is None else ws.numel(),
+                                  _stream(stream)), "moe_norm_backward")
+
+
+def norm_residual_forward(p: NormParams, resid, y, out, weight=None, bias=None, gate=None, mean=None, rstd=None,
+                          next_weight=None, next_bias=None, x_next=None, q8=None, s8=None, next_mean=None,
+                          next_rstd=None, stream=None):
+    """moe_norm_residual_forward: out = alpha resid + beta gate N(y), and x_next = N2(out) with p.next_kind."""
+    f32, par = _dtypes(DT_F32), _dtypes(p.param_dtype)
+    row, st, bl, tok, vec = (p.T, p.d), _dtypes(p.stream_dtype), _dtypes(p.block_dtype), (p.T,), (p.d,)
+    _fits("moe_norm_residual_forward", stream, ("resid", resid, row, st, False), ("y", y, row, bl, False),
+          ("out", out, row, st, False), ("x_next", x_next, row, bl, False), ("weight", weight, vec, par, True),
+          ("bias", bias, vec, par, True), ("gate", gate, tok if p.gate_kind == GATE_TOKEN else vec, par, True),
+          ("next_weight", next_weight, vec, par, True), ("next_bias", next_bias, vec, par, True),
+          ("q8", q8, row, _dtypes(DT_E4M3), True), ("s8", s8, ((p.d + 127) // 128, p.T), f32, True),
+          ("mean", mean, tok, f32, True), ("rstd", rstd, tok, f32, True), ("next_mean", next_mean, tok, f32, True),
+          ("next_rstd", next_rstd, tok, f32, True))
+    _rows_ok("moe_norm_residual_forward", p, p.ld_stream, resid=resid, out=out)
+    _rows_ok("moe_norm_residual_forward", p, p.ld_block, y=y, x_next=x_next)
+    check(lib().moe_norm_residual_forward(ctypes.byref(p), _p(resid), _p(y), _p(weight), _p(bias), _p(gate), _p(out),
+                                          _p(mean), _p(rstd), _p(next_weight), _p(next_bias), _p(x_next), _p(q8),
+                                          _p(s8), _p(next_mean), _p(next_rstd), _stream(stream)),
+          "moe_norm_residual_forward")
+
+
+def norm_residual_backward(p: NormParams, y, dout, mean, rstd, dy, ws=None, weight=None, bias=None, gate=None,
+                           dresid=None, dw=None, db=None, dgate=None, stream=None):
+    """moe_norm_residual_backward: gradients of norm_residual_forward's out. ws: norm_workspace(p)."""
+    f32, par = _dtypes(DT_F32), _dtypes(p.param_dtype)
+    row, st, bl, tok, vec = (p.T, p.d), _dtypes(p.stream_dtype), _dtypes(p.block_dtype), (p.T,), (p.d,)
+    g = tok if p.gate_kind == GATE_TOKEN else vec
+    _fits("moe_norm_residual_backward", stream, ("y", y, row, bl, False), ("dout", dout, row, st, False),
+          ("dresid", dresid, row, st, False), ("dy", dy, row, bl, False), ("weight", weight, vec, par, True),
+          ("bias", bias, vec, par, True), ("gate", gate, g, par, True), ("mean", mean, tok, f32, True),
+          ("rstd", rstd, tok, f32, True), ("dw", dw, vec, f32, True), ("db", db, vec, f32, True),
+          ("dgate", dgate, g, f32, True))
+    _rows_ok("moe_norm_residual_backward", p, p.ld_stream, dout=dout, dresid=dresid)
+    _rows_ok("moe_norm_residual_backward", p, p.ld_block, y=y, dy=dy)
+    check(lib().moe_norm_residual_backward(ctypes.byref(p), _p(y), _p(weight), _p(bias), _p(gate), _p(dout), _p(mean),
+                                           _p(rstd), _p(dresid), _p(dy), ctypes.byref(_norm_grads(dw, db, dgate)),
+                                           _p(ws), 0 if ws is None else ws.numel(), _stream(stream)),
+          "moe_norm_residual_backward")
+
+
+# ------------------------------------------------------------------ products in 8-bit floating point
+
+def f8_params(rows, K, N, E=1, out_dtype=DT_BF16, swiglu_limit=0.0, variant=VARIANT_AUTO) -> F8Params:
+    return F8Params(rows, K, N, E, out_dtype, swiglu_limit, variant)
+
+
+def f8_workspace(p: F8Params, device="cuda"):
+    """A zeroed device workspace for matmul_f8 and gated_f8 (256-byte aligned)."""
+    import torch
+    n = int(lib().moe_f8_workspace_size(ctypes.byref(p)))
+    if n == 0:
+        raise MoeError("invalid parameters")
+    ws = torch.zeros(n, dtype=torch.uint8, device=device)
+    assert ws.data_ptr() % 256 == 0
+    return ws
+
+
+def quantize_f8(x, q, s, ws, row_index=None, n_rows=None, stream=None):
+    """moe_quantize_f8: rows of x (x[row_index] when given) to e4m3 q [rows, K] and scales s [ceil(K/128), rows].
+    ws: 256 zeroed bytes (the error word); n_rows: device int32, rows from it on are left as they were."""
+    import torch
+    rows, K = q.shape
+    _fits("moe_quantize_f8", stream, ("x", x, (x.shape[0], K), (torch.float32, torch.bfloat16, torch.float16), False),
+          ("q", q, (rows, K), _dtypes(DT_E4M3), True), ("s", s, ((K + 127) // 128, rows), (torch.float32,), True),
+          ("row_index", row_index, (rows,), (torch.int32,), True),
+          ("n_rows", n_rows, () if n_rows is None else n_rows.shape, (torch.int32,), True),
+          ("ws", ws, ws.shape, (torch.uint8,), True))
+    if x.shape[0] > 0 and (K > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < K):
+        raise MoeError(f"moe_quantize_f8: x has strides {x.stride()}")
+    check(lib().moe_quantize_f8(rows, K, _p(x), _dt(x), x.stride(0) if x.shape[0] > 1 else K, x.shape[0],
+                                _p(row_index), _p(n_rows), _p(q), _p(s), _p(ws), ws.numel(), _stream(stream)),
+          "moe_quantize_f8")
+
+
+def quantize_f8_weights(w, q, s, transposed=False, stream=None):
+    """moe_quantize_f8_weights: w [E, N, K] ([E, K, N] with transposed) to e4m3 q [E, N, K] and its block scales."""
+    import torch
+    E, N, K = q.shape
+    _fits("moe_quantize_f8_weights", stream,
+          ("w", w, (E, K, N) if transposed else (E, N, K), (torch.float32, torch.bfloat16, torch.float16), True),
+          ("q", q, (E, N, K), _dtypes(DT_E4M3), True),
+          ("s", s, (E, (N + 127) // 128, (K + 127) // 128), (torch.float32,), True))
+    check(lib().moe_quantize_f8_weights(E, N, K, _p(w), _dt(w), int(bool(transposed)), _p(q), _p(s),
+                                        _stream(stream)), "moe_quantize_f8_weights")
+
+
+def _f8_operands(what, stream, p, a, a_scale, offsets, ws, *more):
+    import torch
+    f8, f32 = _dtypes(DT_E4M3), (torch.float32,)
+    kb, nb = (p.K + 127) // 128, (p.N + 127) // 128
+    named = []
+    for name, t in more:
+        named.append((name, t, (p.E, p.N, p.K), f8, True) if not name.startswith("scale of ") else
+                     (name, t, (p.E, nb, kb), f32, True))
+    _fits(what, stream, ("a", a, (p.rows, p.K), f8, True), ("a_scale", a_scale, (kb, p.rows), f32, True),
+          ("offsets", offsets, (p.E + 1,), (torch.int32,), True), ("ws", ws, ws.shape, (torch.uint8,), True), *named)
+
+
+def matmul_f8(p: F8Params, a, a_scale, b, b_scale, out, ws, offsets=None, sorted_pair=None, topk_w=None, stream=None):
+    """moe_matmul_f8: out = w_r * a b^T by expert, e4m3 with scales for each block of 128."""
+    import torch
+    _f8_operands("moe_matmul_f8", stream, p, a, a_scale, offsets, ws, ("b", b), ("scale of b", b_scale))
+    _fits("moe_matmul_f8", stream, ("out", out, (p.rows, p.N), _dtypes(p.out_dtype), True),
+          ("sorted_pair", sorted_pair, (p.rows,), (torch.int32,), True),
+          ("topk_w", topk_w, () if topk_w is None else topk_w.shape, (torch.float32,), True))
+    check(lib().moe_matmul_f8(ctypes.byref(p), _p(a), _p(a_scale), _p(offsets), _p(b), _p(b_scale), _p(sorted_pair),
+                              _p(topk_w), _p(out), _p(ws), ws.numel(), _stream(stream)), "moe_matmul_f8")
+
+
+def gated_f8(p: F8Params, a, a_scale, w_gate, s_gate, w_up, s_up, h, ws, h_scale=None, offsets=None, stream=None):
+    """moe_gated_f8: h = silu(clamp(a w_gate^T)) * clamp(a w_up^T) by expert; e4m3 h with h_scale."""
+    import torch
+    _f8_operands("moe_gated_f8", stream, p, a, a_scale, offsets, ws, ("w_gate", w_gate), ("scale of w_gate", s_gate),
+                 ("w_up", w_up), ("scale of w_up", s_up))
+    _fits("moe_gated_f8", stream, ("h", h, (p.rows, p.N), _dtypes(p.out_dtype), True),
+          ("h_scale", h_scale, ((p.N + 127) // 128, p.rows), (torch.float32,), True))
+    check(lib().moe_gated_f8(ctypes.byref(p), _p(a), _p(a_scale), _p(offsets), _p(w_gate), _p(s_gate), _p(w_up),
+                             _p(s_up), _p(h), _p(h_scale), _p(ws), ws.numel(), _stream(stream)), "moe_gated_f8")

@@ -41,6 +41,8 @@ int num_sms() {
     return cached[dev];
 }
 
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+
 static size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 // Host-side checks of moe_params; fills D. Returns MOE_OK or an error code.
@@ -296,7 +298,7 @@ static int status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR
 
 extern "C" {
 
-int moe_version(void) { return 100; }
+int moe_version(void) { return 101; }
 
 const char* moe_status_string(int s) {
     switch (s) {

@@ -1,0 +1,115 @@
+// f8.cu — entry points of the products in 8-bit floating point: argument checks and
+// the choice between the streaming kernels (f8_stream.cu) and the tiles (f8_tile.cu).
+#include "f8.cuh"
+
+namespace moe {
+
+namespace f8 {
+
+namespace {
+
+bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int check_params(const moe_f8_params* p) {
+    if (!p || p->rows < 0 || p->rows >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    if (p->K < 16 || p->K % 16 || p->N < 8 || p->N % 8 || p->E < 1 || p->E > kMaxE) return MOE_ERR_INVALID_ARG;
+    if (p->out_dtype < MOE_DT_F32 || p->out_dtype > MOE_DT_E4M3) return MOE_ERR_INVALID_ARG;
+    if (p->variant < MOE_VARIANT_AUTO || p->variant > MOE_VARIANT_STREAM) return MOE_ERR_INVALID_ARG;
+    if (!(p->swiglu_limit >= -3.4e38f && p->swiglu_limit <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
+    // weight rows and scale blocks are counted in 32 bits
+    if (int64_t(p->N) * p->E >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    if (int64_t((p->N + 127) / 128) * ((p->K + 127) / 128) * p->E >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+int check_call(const moe_f8_params* p, const uint8_t* a, const float* a_scale, const int32_t* offsets, const void* out,
+               const void* ws, size_t ws_bytes) {
+    if (!ws) return MOE_ERR_INVALID_ARG;
+    if (!al(ws, 256)) return MOE_ERR_MISALIGNED;
+    if (ws_bytes < moe_f8_workspace_size(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (p->rows == 0) return MOE_OK;
+    if (!a || !a_scale || !out || (p->E > 1 && !offsets)) return MOE_ERR_INVALID_ARG;
+    if (!al(a, 16) || !al(a_scale, 4) || !al(offsets, 4) || !al(out, 16)) return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+int check_weights(const uint8_t* b, const float* s) {
+    if (!b || !s) return MOE_ERR_INVALID_ARG;
+    return al(b, 16) && al(s, 4) ? MOE_OK : MOE_ERR_MISALIGNED;
+}
+
+Args args_of(const moe_f8_params* p, const uint8_t* a, const float* a_scale, const int32_t* offsets, void* out,
+             void* ws) {
+    Args x{};
+    x.a = a;
+    x.a_scale = a_scale;
+    x.offsets = offsets;
+    x.out = out;
+    x.rows = p->rows;
+    x.K = p->K;
+    x.N = p->N;
+    x.E = p->E;
+    x.KB = (p->K + 127) / 128;
+    x.NB = (p->N + 127) / 128;
+    x.out_dt = p->out_dtype;
+    x.limit = p->swiglu_limit;
+    x.err = static_cast<uint32_t*>(ws);
+    x.wait_ns = wait_limit_ns();
+    return x;
+}
+
+int launch(const moe_f8_params* p, const Args& x, bool gated, cudaStream_t s) {
+    return launch_stream(x, gated, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+}  // namespace f8
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_f8_workspace_size(const moe_f8_params* p) { return f8::check_params(p) == MOE_OK ? 256 : 0; }
+
+int moe_matmul_f8(const moe_f8_params* p, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                  const uint8_t* b, const float* b_scale, const int32_t* sorted_pair, const float* topk_w, void* out,
+                  void* ws, size_t ws_bytes, moe_stream_t stream) {
+    int st = f8::check_params(p);
+    if (st != MOE_OK) return st;
+    if (p->out_dtype == MOE_DT_E4M3) return MOE_ERR_UNSUPPORTED;  // its 128 columns' scale is the gated form's
+    if ((st = f8::check_call(p, a, a_scale, offsets, out, ws, ws_bytes)) != MOE_OK || p->rows == 0) return st;
+    if ((st = f8::check_weights(b, b_scale)) != MOE_OK) return st;
+    if (!sorted_pair != !topk_w) return MOE_ERR_INVALID_ARG;
+    if (!f8::al(sorted_pair, 4) || !f8::al(topk_w, 4)) return MOE_ERR_MISALIGNED;
+    f8::Args x = f8::args_of(p, a, a_scale, offsets, out, ws);
+    x.b[0] = x.b[1] = b;
+    x.b_scale[0] = x.b_scale[1] = b_scale;
+    x.sorted_pair = sorted_pair;
+    x.topk_w = topk_w;
+    return f8::launch(p, x, false, stream);
+}
+
+int moe_gated_f8(const moe_f8_params* p, const uint8_t* a, const float* a_scale, const int32_t* offsets,
+                 const uint8_t* w_gate, const float* s_gate, const uint8_t* w_up, const float* s_up, void* h,
+                 float* h_scale, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    int st = f8::check_params(p);
+    if (st != MOE_OK) return st;
+    const bool e4m3 = p->out_dtype == MOE_DT_E4M3;
+    if (e4m3 && p->N % 16) return MOE_ERR_INVALID_ARG;
+    if ((st = f8::check_call(p, a, a_scale, offsets, h, ws, ws_bytes)) != MOE_OK || p->rows == 0) return st;
+    if ((st = f8::check_weights(w_gate, s_gate)) != MOE_OK || (st = f8::check_weights(w_up, s_up)) != MOE_OK) return st;
+    if (e4m3 != (h_scale != nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!f8::al(h_scale, 4)) return MOE_ERR_MISALIGNED;
+    f8::Args x = f8::args_of(p, a, a_scale, offsets, h, ws);
+    x.b[0] = w_gate;
+    x.b[1] = w_up;
+    x.b_scale[0] = s_gate;
+    x.b_scale[1] = s_up;
+    x.h_scale = h_scale;
+    return f8::launch(p, x, true, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,184 @@
+// f8_stream.cu — the 8-bit products for a few rows (single tokens): every weight
+// byte is read once, straight into registers, and the time is HBM's.
+//
+// A block takes 16 columns of the result (16 rows of the K-major weights, of both
+// projections when gated) and up to 8 rows of one expert; its 8 warps take every
+// eighth block of 128 along K. A lane loads 16 bytes of weights at a time; they
+// are the A operand of mma.sync m16n8k32 (e4m3) as they come: the fragment wants
+// 4 bytes of K at tig*4 and at 16 + tig*4, but a sum over K may take K in any order,
+// so lane tig holds bytes 16 tig.. of a 64-byte piece and feeds them to two products,
+// with the same bytes of the 8 rows as the B operand. Nothing passes through shared
+// memory. A block of 128 is summed from zero, multiplied by its two scales and added
+// in fp32; the 8 warps' sums are added in order at the end (no atomics).
+// Gated with e4m3 results needs the largest of 128 columns: the 8 blocks that hold
+// them are one cluster and exchange their maxima through its shared memory.
+#include <algorithm>
+
+#include "f8.cuh"
+
+namespace moe {
+
+namespace f8 {
+
+namespace {
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kCols = 16;   // columns of the result per block
+constexpr int kRows = 8;    // rows per block
+constexpr int kGroup = 8;   // blocks per 128 columns: the cluster of the e4m3 form
+
+MOE_DEV void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+MOE_DEV uint4 ld_weights(const uint8_t* p, bool in) {
+    // read once: past L1
+    return in ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+}
+
+template <bool GATED, bool E4M3>
+__global__ void __launch_bounds__(kThreads) f8_stream_kernel(const Args p) {
+    constexpr int M = GATED ? 2 : 1;
+    __shared__ int found[12];
+    __shared__ float part[kWarps][M][kRows][kCols + 1];
+    __shared__ uint32_t amax[kRows];
+    griddep_wait();
+    griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+    const int n0 = blockIdx.x * kCols;
+    int e, nr;
+    int64_t row0;
+    // the same chunks of rows for every block of a cluster: they leave together
+    for (int u = blockIdx.y; find_rows(p, u, kRows, found, e, row0, nr); u += gridDim.y) {
+
+        float acc[M][4];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
+        const bool in0 = n0 + gid < p.N, in1 = n0 + 8 + gid < p.N, inr = gid < nr;
+        const int64_t w0 = (int64_t(e) * p.N + n0 + gid) * p.K + tig * 16;
+        const int64_t w8 = w0 + int64_t(8) * p.K;
+        const uint8_t* arow = p.a + (row0 + gid) * p.K + tig * 16;
+        const int r0 = min(2 * tig, nr - 1), r1 = min(2 * tig + 1, nr - 1);  // columns of the product past nr are not kept
+        const int sb0 = (e * p.NB + n0 / 128) * p.KB;
+#pragma unroll 2
+        for (int kb = warp; kb < p.KB; kb += kWarps) {
+            const int k = kb * 128;
+            const bool ka = k + tig * 16 < p.K, kc = k + 64 + tig * 16 < p.K;
+            uint4 w[M][4], x[2];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                w[m][0] = ld_weights(p.b[m] + w0 + k, in0 && ka);
+                w[m][1] = ld_weights(p.b[m] + w8 + k, in1 && ka);
+                w[m][2] = ld_weights(p.b[m] + w0 + k + 64, in0 && kc);
+                w[m][3] = ld_weights(p.b[m] + w8 + k + 64, in1 && kc);
+            }
+            x[0] = inr && ka ? __ldg(reinterpret_cast<const uint4*>(arow + k)) : make_uint4(0, 0, 0, 0);
+            x[1] = inr && kc ? __ldg(reinterpret_cast<const uint4*>(arow + k + 64)) : make_uint4(0, 0, 0, 0);
+            const float* as = p.a_scale + int64_t(kb) * p.rows + row0;
+            const float s0 = __ldg(as + r0), s1 = __ldg(as + r1);
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const float sb = __ldg(p.b_scale[m] + sb0 + kb);
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    mma_e4m3(c, w[m][2 * h].x, w[m][2 * h + 1].x, w[m][2 * h].y, w[m][2 * h + 1].y, x[h].x, x[h].y);
+                    mma_e4m3(c, w[m][2 * h].z, w[m][2 * h + 1].z, w[m][2 * h].w, w[m][2 * h + 1].w, x[h].z, x[h].w);
+                }
+                acc[m][0] = fmaf(c[0], sb * s0, acc[m][0]);
+                acc[m][1] = fmaf(c[1], sb * s1, acc[m][1]);
+                acc[m][2] = fmaf(c[2], sb * s0, acc[m][2]);
+                acc[m][3] = fmaf(c[3], sb * s1, acc[m][3]);
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+            part[warp][m][2 * tig][gid] = acc[m][0];
+            part[warp][m][2 * tig + 1][gid] = acc[m][1];
+            part[warp][m][2 * tig][gid + 8] = acc[m][2];
+            part[warp][m][2 * tig + 1][gid + 8] = acc[m][3];
+        }
+        __syncthreads();
+        // one value a thread: row i / 16, column i % 16
+        const int i = threadIdx.x, r = i / kCols, c = i % kCols;
+        float v = 0.f;
+        if (i < kRows * kCols) {
+            float s[M];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                s[m] = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) s[m] += part[w][m][r][c];
+            }
+            if constexpr (GATED) v = gated(s[0], s[1], p.limit);
+            else v = s[0];
+        }
+        const bool keep = i < kRows * kCols && r < nr && n0 + c < p.N;
+        if constexpr (!E4M3) {
+            if (keep) {
+                if constexpr (!GATED) v *= row_weight(p, row0 + r);
+                store_out(p, row0 + r, n0 + c, v);
+            }
+        } else {
+            // the row's largest of these 16 columns, then of the cluster's 128
+            uint32_t m = keep ? abs_bits(v) : 0u;
+#pragma unroll
+            for (int o = 1; o < kCols; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            if (i < kRows * kCols && c == 0) amax[r] = m;
+            cluster_sync_all();
+            if (i < kRows * kCols) {
+                const uint32_t mine = smem_u32(&amax[r]);
+#pragma unroll
+                for (int b = 0; b < kGroup; ++b) {
+                    uint32_t o;
+                    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(o) : "r"(mapa_shared(mine, b)));
+                    m = max(m, o);
+                }
+            }
+            cluster_sync_all();  // no block leaves while another reads its maxima
+            if (keep) {
+                const float sc = f8_scale(m);
+                const F8Div div(sc);
+                static_cast<uint8_t*>(p.out)[(row0 + r) * p.N + n0 + c] =
+                    uint8_t(pack_e4m3x2(div.fast ? div(v) : __fdiv_rn(v, sc), 0.f) & 0xFFu);
+                if (n0 % 128 == 0 && c == 0) p.h_scale[int64_t(n0 / 128) * p.rows + row0 + r] = sc;
+            }
+        }
+        __syncthreads();  // found, part and amax are written anew
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_stream(const Args& p, bool gated, cudaStream_t s) {
+    const bool e4m3 = p.out_dt == MOE_DT_E4M3;
+    // at most one partial chunk an expert beside the full ones
+    const int64_t chunks = p.offsets ? std::min<int64_t>(p.rows, p.E) + p.rows / kRows : (p.rows + kRows - 1) / kRows;
+    const int strips = e4m3 ? p.NB * kGroup : (p.N + kCols - 1) / kCols;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = use_pdl(p.rows) ? 1 : 0;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kGroup;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = e4m3 ? 2 : 1;
+    cfg.gridDim = dim3(strips, unsigned(std::min<int64_t>(chunks, 65535)));
+    ProfScope prof_(MOE_K_STREAM_F8, s);
+    return !gated ? cudaLaunchKernelEx(&cfg, f8_stream_kernel<false, false>, p)
+           : e4m3 ? cudaLaunchKernelEx(&cfg, f8_stream_kernel<true, true>, p)
+                  : cudaLaunchKernelEx(&cfg, f8_stream_kernel<true, false>, p);
+}
+
+}  // namespace f8
+
+}  // namespace moe

@@ -172,6 +172,8 @@ cudaError_t launch_backward(const Dims& D, const BwdArgs& a, cudaStream_t s);
 
 // ---- device properties, cached per device
 int num_sms();
+// Limit of the bounded waits (moe_set_wait_limit_ns).
+uint64_t wait_limit_ns();
 
 // Programmatic stream serialization (see griddep_wait) pays off only when the
 // layer's kernels are short: measured on B200, it saved ~2 us of a 106 us
