@@ -59,7 +59,8 @@ Args args_of(const moe_f8_params* p, const uint8_t* a, const float* a_scale, con
 }
 
 int launch(const moe_f8_params* p, const Args& x, bool gated, cudaStream_t s) {
-    return launch_stream(x, gated, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    const bool stream = p->variant == MOE_VARIANT_STREAM || (p->variant == MOE_VARIANT_AUTO && p->rows <= 16);
+    return (stream ? launch_stream(x, gated, s) : launch_tile(x, gated, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
