@@ -1,5 +1,7 @@
 // f8.cu — entry points of the products in 8-bit floating point: argument checks and
 // the choice between the streaming kernels (f8_stream.cu) and the tiles (f8_tile.cu).
+#include <limits>
+
 #include "f8.cuh"
 
 namespace moe {
@@ -52,7 +54,7 @@ Args args_of(const moe_f8_params* p, const uint8_t* a, const float* a_scale, con
     x.KB = (p->K + 127) / 128;
     x.NB = (p->N + 127) / 128;
     x.out_dt = p->out_dtype;
-    x.limit = p->swiglu_limit;
+    x.limit = p->swiglu_limit > 0.f ? p->swiglu_limit : std::numeric_limits<float>::infinity();
     x.err = static_cast<uint32_t*>(ws);
     x.wait_ns = wait_limit_ns();
     return x;

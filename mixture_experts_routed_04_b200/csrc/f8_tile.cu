@@ -37,11 +37,12 @@ namespace {
 constexpr int BM = 128, BN = 256, BK = 128;
 constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
 constexpr int STAGES = 4;
-constexpr int EPI = 8, THREADS = 32 * (2 + EPI);
-constexpr int PIECE = 32 * 64;  // a warp's turn buffer: 32 rows of 64 bytes
-constexpr int OFF_TURN = STAGES * STAGE;
-constexpr int OFF_MISC = OFF_TURN + EPI * PIECE;
-constexpr int MISC = 4096;
+constexpr int EPI = 8, FIRST = 4, THREADS = 32 * (FIRST + EPI);
+constexpr int PARTS = EPI / 4;      // column parts of a tile; the warps of a lane quadrant
+constexpr int CW = BN / PARTS;      // columns of the accumulator a thread
+constexpr int OFF_MISC = STAGES * STAGE;
+constexpr int SLOTS = 8;         // blocks whose scales are on their way
+constexpr int MISC = 11 * 1024;
 constexpr int SMEM = 1024 + OFF_MISC + MISC;
 static_assert(SMEM <= 232448, "dynamic shared memory a block may opt into");
 
@@ -57,16 +58,47 @@ MOE_DEV void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t
         : "memory");
 }
 
+// Registers of a warpgroup from here on. The launch gives 12 warps 168 each; the split's sum,
+// 4 x 40 + 8 x 232 a lane, is the same.
+template <int N>
+MOE_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+MOE_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+MOE_DEV void ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+MOE_DEV void wait16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
+}
 struct Misc {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t tfull[2], tempty[2];
+    uint64_t sfull[SLOTS], sempty[SLOTS];
+    uint64_t ufull[2], uempty[2];
     uint64_t xch[4];      // the two warps of a lane quadrant
     uint64_t drain;
     uint32_t tmem;
     int abort;
     int found[12];
     int base[kMaxE + 1];          // exclusive prefix of the experts' M-tiles
-    uint32_t amax[2][2][BM];      // [unit parity][column half][row]
+    int off[kMaxE + 1];           // their row offsets
+    float sa[SLOTS][BM];          // the rows' scales of a block
+    float sb[SLOTS][2];           // the weights': of the tile's two 128-column halves, or gate and up
+    int64_t urow0[2];             // by unit parity: what the tile's results need
+    int urows[2], un[2];
+    float uw[2][BM];              // the rows' gate weights
+    uint32_t amax[2][PARTS][BM];  // [unit parity][column part][row]
 };
 static_assert(sizeof(Misc) <= MISC, "barriers, tile prefix and maxima fit their place");
 
@@ -75,8 +107,9 @@ struct Unit {
     int64_t row0;
 };
 
-MOE_DEV Unit unit_of(int u, int nt, const Args& p, const int* base) {
+MOE_DEV Unit unit_of(int u, int nt, const Args& p, const Misc* ms) {
     Unit U;
+    const int* base = ms->base;
     const int g = u / nt;  // as if every M-tile had its n-tiles next to each other: the expert is the same
     int lo = 0, hi = p.E;  // base[lo] <= g < base[hi]
     while (hi - lo > 1) {
@@ -88,12 +121,44 @@ MOE_DEV Unit unit_of(int u, int nt, const Args& p, const int* base) {
     const int mt = base[lo + 1] - base[lo], local = u - base[lo] * nt;
     U.n = local / mt;
     const int m = local - U.n * mt;
-    const int64_t off = p.offsets ? __ldg(p.offsets + lo) : 0;
-    const int64_t end = p.offsets ? __ldg(p.offsets + lo + 1) : p.rows;
-    U.row0 = off + int64_t(m) * BM;
-    U.rows = int(min(int64_t(BM), end - U.row0));
+    U.row0 = ms->off[lo] + int64_t(m) * BM;
+    U.rows = int(min(int64_t(BM), ms->off[lo + 1] - U.row0));
     return U;
 }
+
+MOE_DEV void st_global_32(void* p, const uint4& lo, const uint4& hi) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+                 "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+                 : "memory");
+}
+// Eight values to 16 bits; sixteen in units of a scale to e4m3.
+MOE_DEV uint4 pack8_at(const float* x, bool bf16) {
+    return bf16 ? make_uint4(cvt_bf16x2(x[0], x[1]), cvt_bf16x2(x[2], x[3]), cvt_bf16x2(x[4], x[5]), cvt_bf16x2(x[6], x[7]))
+                : make_uint4(pack_f16x2(x[0], x[1]), pack_f16x2(x[2], x[3]), pack_f16x2(x[4], x[5]), pack_f16x2(x[6], x[7]));
+}
+MOE_DEV uint4 pack16_e4m3(const float* x, const F8Div& div) {
+    uint32_t w[4];
+    if (div.fast) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack_e4m3x2(div(x[4 * i]), div(x[4 * i + 1])) | pack_e4m3x2(div(x[4 * i + 2]), div(x[4 * i + 3])) << 16;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = pack_e4m3x2(__fdiv_rn(x[4 * i], div.s), __fdiv_rn(x[4 * i + 1], div.s)) |
+                   pack_e4m3x2(__fdiv_rn(x[4 * i + 2], div.s), __fdiv_rn(x[4 * i + 3], div.s)) << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 4 bytes global -> shared, asynchronous; the thread's arrival on bar once its copies have landed.
+MOE_DEV void cp_async_4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+MOE_DEV void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+MOE_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Every lane waits; warp-uniform result.
 MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, Misc* m, const Args& p) {
@@ -101,7 +166,7 @@ MOE_DEV bool warp_wait(uint64_t* bar, uint32_t parity, Misc* m, const Args& p) {
     return __all_sync(0xFFFFFFFFu, ok);
 }
 
-template <bool GATED>
+template <bool GATED, int OUT>
 __global__ void __launch_bounds__(THREADS, 1)
     f8_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
                    const __grid_constant__ CUtensorMap tmB1, const Args p) {
@@ -118,7 +183,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(ms->tfull + a, 1);
             mbar_init(ms->tempty + a, EPI);
         }
-        for (int q = 0; q < 4; ++q) mbar_init(ms->xch + q, 2);
+        for (int q = 0; q < 4; ++q) mbar_init(ms->xch + q, PARTS);
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(ms->ufull + a, 32);
+            mbar_init(ms->uempty + a, EPI);
+        }
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(ms->sfull + i, 32);
+            mbar_init(ms->sempty + i, EPI);
+        }
         mbar_init(&ms->drain, 1);
         ms->abort = 0;
         fence_mbar_init();
@@ -139,9 +212,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int t = threadIdx.x;
         int cnt = 0;
         if (!p.offsets) {
-            if (t == 0) cnt = int((p.rows + BM - 1) / BM);
+            if (t == 0) {
+                cnt = int((p.rows + BM - 1) / BM);
+                ms->off[0] = 0;
+                ms->off[1] = int(p.rows);
+            }
         } else if (t < p.E) {
             const int off = __ldg(p.offsets + t), end = __ldg(p.offsets + t + 1);
+            ms->off[t] = off;
+            if (t == p.E - 1) ms->off[t + 1] = end;
             if (off < 0 || end < off || end > p.rows) set_error(p.err, MOE_DEVERR_BOUNDS);  // not followed
             else cnt = (end - off + BM - 1) / BM;
         }
@@ -165,22 +244,21 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int nt = (p.N + cols - 1) / cols;
     const int total = ms->base[p.E] * nt;
 
+    if (warp < FIRST) {
+        reg_dec<40>();
     if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        int stage = 0;
-        uint32_t phase = 0, issued = 0, issued_par = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-            const Unit U = unit_of(u, nt, p, ms->base);
-            for (int kb = 0; kb < p.KB; ++kb) {
-                int okl = 1;
-                if (lane == 0) okl = mbar_wait_bounded(ms->empty + stage, phase ^ 1u, &ms->abort, p.err, p.wait_ns);
-                okl = __shfl_sync(0xFFFFFFFFu, okl, 0);
-                if (!okl) {
-                    ok = false;
-                    break;
-                }
-                if (lane == 0) {
+        // ------------------------------------------------ TMA producer (one thread)
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued = 0, issued_par = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+                const Unit U = unit_of(u, nt, p, ms);
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!mbar_wait_bounded(ms->empty + stage, phase ^ 1u, &ms->abort, p.err, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
                     uint8_t* sa = smem + stage * STAGE;
                     mbar_arrive_expect_tx(ms->full + stage, STAGE);
                     tma_load_2d(sa, &tmA, ms->full + stage, kb * BK, int(U.row0));
@@ -192,93 +270,129 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     issued |= 1u << stage;
                     issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-                }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
-        }
-        // on abort, every copy already issued lands before the CTA can exit
-        if (!ok && lane == 0) {
-            for (int s = 0; s < STAGES; ++s)
-                if (issued >> s & 1u) mbar_wait_bounded(ms->full + s, (issued_par >> s) & 1u, nullptr, p.err, kDrainLimitNs);
+            // on abort, every copy already issued lands before the CTA can exit
+            if (!ok)
+                for (int s = 0; s < STAGES; ++s)
+                    if (issued >> s & 1u) mbar_wait_bounded(ms->full + s, (issued_par >> s) & 1u, nullptr, p.err, kDrainLimitNs);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer
-        int stage = 0, acc = 0;
-        uint32_t phase = 0, acc_phase = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-            for (int kb = 0; kb < p.KB; ++kb) {
-                int okl = 1;
-                if (lane == 0) {
-                    okl = mbar_wait_bounded(ms->tempty + acc, acc_phase ^ 1u, &ms->abort, p.err, p.wait_ns) &&
-                          mbar_wait_bounded(ms->full + stage, phase, &ms->abort, p.err, p.wait_ns);
-                    if (okl) {
-                        tc_fence_after();
-                        const uint32_t a0 = smem_u32(smem + stage * STAGE), b0 = a0 + A_BYTES;
-#pragma unroll
-                        for (int j = 0; j < BK / 32; ++j)  // 32 bytes of K inside the swizzled rows
-                            umma_f8(tmem_base + uint32_t(acc * BN), sdesc_sw128(a0 + j * 32, 16, 1024),
-                                    sdesc_sw128(b0 + j * 32, 16, 1024), j != 0);
-                        umma_commit(ms->empty + stage);
-                        umma_commit(ms->tfull + acc);
+        // ------------------------------------------------ MMA issuer (one thread)
+        if (lane == 0) {
+            const uint64_t da = sdesc_sw128(smem_u32(smem), 16, 1024), db = sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
+            int stage = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!mbar_wait_bounded(ms->full + stage, phase, &ms->abort, p.err, p.wait_ns) || !mbar_wait_bounded(ms->tempty + acc, acc_phase ^ 1u, &ms->abort, p.err, p.wait_ns)) {
+
+                        ok = false;
+                        break;
                     }
-                }
-                okl = __shfl_sync(0xFFFFFFFFu, okl, 0);
-                if (!okl) {
-                    ok = false;
-                    break;
-                }
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-                if (++acc == 2) {
-                    acc = 0;
-                    acc_phase ^= 1u;
+                    tc_fence_after();
+                    // addresses in the descriptors are in units of 16 bytes, below 2^14
+                    const uint64_t so = uint64_t(stage * (STAGE / 16));
+#pragma unroll
+                    for (int j = 0; j < BK / 32; ++j)  // 32 bytes of K inside the swizzled rows
+                        umma_f8(tmem_base + uint32_t(acc * BN), da + so + j * 2, db + so + j * 2, j != 0);
+                    umma_commit(ms->tfull + acc);
+                    umma_commit(ms->empty + stage);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    acc ^= 1;
+                    if (acc == 0) acc_phase ^= 1u;
                 }
             }
-        }
-        // every MMA this thread issued has completed before TMEM is freed
-        if (lane == 0) {
+            // every MMA this thread issued has completed before TMEM is freed
             umma_commit(&ms->drain);
             mbar_wait_bounded(&ms->drain, 0, nullptr, p.err, kDrainLimitNs);
         }
         __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------ scales
+        // A block's 128 row scales and 2 weight scales, 8 blocks ahead: loaded by the warps
+        // that use them, a block ahead, their latency under load was longer than a block.
+        int slot = 0, par = 0;
+        uint32_t phase = 0, uphase = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+            const Unit U = unit_of(u, nt, p, ms);
+            const float* as[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) as[i] = p.a_scale + U.row0 + min(i * 32 + lane, U.rows - 1);
+            if (!warp_wait(ms->uempty + par, uphase ^ 1u, ms, p)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                ms->urow0[par] = U.row0;
+                ms->urows[par] = U.rows;
+                ms->un[par] = U.n;
+            }
+            if (p.sorted_pair) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ms->uw[par][i * 32 + lane] = row_weight(p, U.row0 + min(i * 32 + lane, U.rows - 1));
+            }
+            mbar_arrive(ms->ufull + par);
+            par ^= 1;
+            if (par == 0) uphase ^= 1u;
+            const int nb = GATED ? U.n : min(U.n * 2 + (lane & 1), p.NB - 1);
+            const float* bs = p.b_scale[GATED ? lane & 1 : 0] + (int64_t(U.e) * p.NB + nb) * p.KB;
+            for (int kb = 0; kb < p.KB; ++kb) {
+                if (!warp_wait(ms->sempty + slot, phase ^ 1u, ms, p)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    cp_async_4(smem_u32(&ms->sa[slot][i * 32 + lane]), as[i] + int64_t(kb) * p.rows);
+                if (lane < 2) cp_async_4(smem_u32(&ms->sb[slot][lane]), bs + kb);
+                cp_async_arrive(ms->sfull + slot);
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        cp_async_wait_all();
+        __syncwarp();
+    }
     } else {
+        reg_inc<232>();
         // ------------------------------------------------ scaled sums and results
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int q = warp & 3, part = (warp - FIRST) >> 2;
         const uint32_t lanes = uint32_t(q * 32) << 16;
-        // columns of the accumulator: matmul 128 in a row; gated 64 of gate, 64 of up
-        const uint32_t c0 = GATED ? half * 64 : half * 128, c1 = GATED ? 128 + half * 64 : half * 128 + 64;
-        uint8_t* turn = smem + OFF_TURN + (warp - 2) * PIECE;
-        int acc = 0, par = 0;
-        uint32_t acc_phase = 0, xph = 0;
+        // columns of the accumulator: matmul CW in a row; gated CW/2 of gate, CW/2 of up
+        const uint32_t c0 = GATED ? part * (CW / 2) : part * CW, c1 = GATED ? 128 + c0 : c0 + CW / 2;
+        int acc = 0, par = 0, slot = 0;
+        uint32_t acc_phase = 0, xph = 0, sph = 0, uphase = 0;
         bool ok = true, range_bad = false;
         for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-            const Unit U = unit_of(u, nt, p, ms->base);
-            const int rt = q * 32 + lane;  // row of the tile
-            const bool live = rt < U.rows;
-            const int64_t row = U.row0 + rt;
-            float2 s[64];
+            float2 s[CW / 2];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) s[i] = make_float2(0.f, 0.f);
-            const float* as = p.a_scale + (live ? row : U.row0);
-            const int nb = GATED ? U.n : min(U.n * 2 + half, p.NB - 1);
-            const float* b0 = p.b_scale[0] + (int64_t(U.e) * p.NB + nb) * p.KB;
-            const float* b1 = GATED ? p.b_scale[1] + (int64_t(U.e) * p.NB + nb) * p.KB : b0;
-            // the scales of a block are loaded a block ahead
-            float sa = __ldg(as), sb0 = __ldg(b0), sb1 = __ldg(b1);
+            for (int i = 0; i < CW / 2; ++i) s[i] = make_float2(0.f, 0.f);
             for (int kb = 0; kb < p.KB; ++kb) {
-                const float f0 = sa * sb0, f1 = sa * sb1;
-                if (kb + 1 < p.KB) {
-                    sa = __ldg(as + int64_t(kb + 1) * p.rows);
-                    sb0 = __ldg(b0 + kb + 1);
-                    if (GATED) sb1 = __ldg(b1 + kb + 1);
-                    else sb1 = sb0;
+                if (!warp_wait(ms->sfull + slot, sph, ms, p)) {
+                    ok = false;
+                    break;
+                }
+                const float sa = ms->sa[slot][q * 32 + lane];
+                const float f0 = sa * ms->sb[slot][GATED ? 0 : part * CW / 128], f1 = GATED ? sa * ms->sb[slot][1] : f0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ms->sempty + slot);
+                if (++slot == SLOTS) {
+                    slot = 0;
+                    sph ^= 1u;
                 }
                 if (!warp_wait(ms->tfull + acc, acc_phase, ms, p)) {
                     ok = false;
@@ -286,46 +400,64 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t tb = tmem_base + lanes + uint32_t(acc * BN);
+                // the next 16 columns are on their way while these are added; the accumulator
+                // is handed back as soon as the last have come
+                uint32_t t[2][16];
+                auto col_of = [&](int c) { return c < CW / 32 ? c0 + c * 16 : c1 + (c - CW / 32) * 16; };
+                ld16(tb + col_of(0), t[0]);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t t[32];
-                    tmem_ld_32x32b_x32(tb + (c < 2 ? c0 + c * 32 : c1 + (c - 2) * 32), t);
-                    tmem_ld_wait();
-                    const float f = c < 2 ? f0 : f1;
+                for (int c = 0; c < CW / 16; ++c) {
+                    wait16(t[c & 1]);
+                    if (c < CW / 16 - 1) {
+                        ld16(tb + col_of(c + 1), t[(c + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ms->tempty + acc);
+                    }
+                    const float f = c < CW / 32 ? f0 : f1;
                     const float2 ff = make_float2(f, f);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        s[c * 16 + i] = __ffma2_rn(make_float2(__uint_as_float(t[2 * i]), __uint_as_float(t[2 * i + 1])),
-                                                   ff, s[c * 16 + i]);
+                    for (int i = 0; i < 8; ++i)
+                        s[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(t[c & 1][2 * i]),
+                                                              __uint_as_float(t[c & 1][2 * i + 1])),
+                                                  ff, s[c * 8 + i]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(ms->tempty + acc);
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1u;
                 }
             }
             if (!ok) break;
-            // ---- the row's values of this thread: n of them from column col0
-            constexpr int NV = GATED ? 64 : 128;
-            const int col0 = GATED ? U.n * 128 + half * 64 : U.n * BN + half * 128;
-            float* v = reinterpret_cast<float*>(s);
-            if (GATED) {
-#pragma unroll
-                for (int i = 0; i < 64; ++i) v[i] = gated(v[i], v[64 + i], p.limit);
-            } else {
-                const float w = live ? row_weight(p, row) : 0.f;
-#pragma unroll
-                for (int i = 0; i < 128; ++i) v[i] *= w;
+            // ---- the row's values of this thread: NV columns from col0 on
+            if (!warp_wait(ms->ufull + par, uphase, ms, p)) {
+                ok = false;
+                break;
             }
-            const int es = p.out_dt == MOE_DT_F32 ? 4 : p.out_dt == MOE_DT_E4M3 ? 1 : 2;
+            const int rt = q * 32 + lane;  // row of the tile
+            const bool live = rt < ms->urows[par];
+            const int64_t row = ms->urow0[par] + rt;
+            const int un = ms->un[par];
+            const float w = !GATED && p.sorted_pair ? ms->uw[par][rt] : 1.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ms->uempty + par);
+            constexpr int NV = GATED ? CW / 2 : CW;
+            const int col0 = GATED ? un * 128 + part * (CW / 2) : un * BN + part * CW;
+            float* v = reinterpret_cast<float*>(s);
+            if constexpr (GATED) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) v[i] = gated(v[i], v[NV + i], p.limit);
+            } else if (p.sorted_pair) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) v[i] *= w;
+            }
+            constexpr int es = OUT == MOE_DT_F32 ? 4 : OUT == MOE_DT_E4M3 ? 1 : 2;
             float sc = 1.f;
-            if (GATED && p.out_dt == MOE_DT_E4M3) {
+            if constexpr (OUT == MOE_DT_E4M3) {
                 uint32_t m = 0;  // columns past N are zeros of zero weights
 #pragma unroll
-                for (int i = 0; i < 64; ++i) m = max(m, abs_bits(v[i]));
-                ms->amax[par][half][rt] = m;
+                for (int i = 0; i < NV; ++i) m = max(m, abs_bits(v[i]));
+                ms->amax[par][part][rt] = m;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(ms->xch + q);
                 if (!warp_wait(ms->xch + q, xph, ms, p)) {
@@ -333,71 +465,48 @@ __global__ void __launch_bounds__(THREADS, 1)
                     break;
                 }
                 xph ^= 1u;
-                m = max(m, ms->amax[par][half ^ 1][rt]);
-                par ^= 1;
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) m = max(m, ms->amax[par][i][rt]);
                 sc = f8_scale(m);
-                if (half == 0 && live) p.h_scale[int64_t(U.n) * p.rows + row] = sc;
+                if (part == 0 && live) p.h_scale[int64_t(un) * p.rows + row] = sc;
             }
-            // pieces of 32 rows x 64 bytes: 16-byte chunk c of row r at r*64 + ((c ^ (r/2)%4) * 16)
-            char* obase = static_cast<char*>(p.out);
-            auto put = [&](int ch, uint4 x) {
-                *reinterpret_cast<uint4*>(turn + lane * 64 + ((ch ^ ((lane >> 1) & 3)) << 4)) = x;
-            };
-            auto flush = [&](int piece) {
-                __syncwarp();
-                const int rr = lane >> 2, ch = lane & 3;
-                const int col = col0 + (piece * 64 + ch * 16) / es;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = i * 8 + rr;
-                    if (q * 32 + r < U.rows && col < p.N)  // rows of the result are multiples of 16 bytes
-                        *reinterpret_cast<uint4*>(obase + ((U.row0 + q * 32 + r) * p.N + col) * es) =
-                            *reinterpret_cast<const uint4*>(turn + r * 64 + ((ch ^ ((r >> 1) & 3)) << 4));
-                }
-                __syncwarp();
-            };
-            if (es == 4) {
-#pragma unroll
-                for (int pc = 0; pc < NV / 16; ++pc) {
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        const float* x = v + pc * 16 + ch * 4;
-                        put(ch, make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                                           __float_as_uint(x[3])));
-                    }
-                    flush(pc);
-                }
-            } else if (es == 2) {
-                const bool bf = p.out_dt == MOE_DT_BF16;
-                if (!bf && live) {
+            const F8Div div(sc);
+            if constexpr (OUT == MOE_DT_F16) {
+                if (live) {
 #pragma unroll
                     for (int i = 0; i < NV; ++i) range_bad |= !f16_range_ok(v[i]) && col0 + i < p.N;
                 }
-#pragma unroll
-                for (int pc = 0; pc < NV / 32; ++pc) {
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        float x[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = v[pc * 32 + ch * 8 + i];
-                        put(ch, pack8(x, bf));
-                    }
-                    flush(pc);
-                }
-            } else if (GATED) {
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    float x[8], y[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] = v[ch * 16 + i];
-                        y[i] = v[ch * 16 + 8 + i];
-                    }
-                    const uint2 lo = pack8_e4m3(x, sc), hi = pack8_e4m3(y, sc);
-                    put(ch, make_uint4(lo.x, lo.y, hi.x, hi.y));
-                }
-                flush(0);
             }
+            // 32 bytes a store: a whole sector of the row, and nothing to wait for (turning the
+            // rows through shared memory for longer pieces kept the warps from the next tile)
+            char* orow = static_cast<char*>(p.out) + (row * p.N + col0) * es;
+            constexpr int per = 32 / es;  // columns of 32 bytes
+            const bool wide = (int64_t(p.N) * es) % 32 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+#pragma unroll
+            for (int c = 0; c < NV / per; ++c) {
+                const float* x = v + c * per;
+                uint4 lo, hi;
+                if constexpr (es == 4) {
+                    lo = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+                    hi = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+                } else if constexpr (es == 2) {
+                    lo = pack8_at(x, OUT == MOE_DT_BF16);
+                    hi = pack8_at(x + 8, OUT == MOE_DT_BF16);
+                } else {
+                    lo = pack16_e4m3(x, div);
+                    hi = pack16_e4m3(x + 16, div);
+                }
+                const int col = col0 + c * per;
+                if (!live || col >= p.N) continue;
+                if (wide) {
+                    st_global_32(orow + c * 32, lo, hi);
+                } else {  // rows of the result are multiples of 16 bytes
+                    *reinterpret_cast<uint4*>(orow + c * 32) = lo;
+                    if (col + per / 2 < p.N) *reinterpret_cast<uint4*>(orow + c * 32 + 16) = hi;
+                }
+            }
+            par ^= 1;
+            if (par == 0) uphase ^= 1u;
         }
         if (range_bad) set_error(p.err, MOE_DEVERR_RANGE);
     }
@@ -408,14 +517,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-template <bool GATED>
+template <bool GATED, int OUT>
 cudaError_t go(const CUtensorMap& A, const CUtensorMap& B0, const CUtensorMap& B1, const Args& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(f8_tile_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(f8_tile_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     const int64_t mt = p.offsets ? std::min<int64_t>(p.rows, p.E) + p.rows / BM : (p.rows + BM - 1) / BM;
     const int64_t units = mt * ((p.N + (GATED ? 127 : BN - 1)) / (GATED ? 128 : BN));
     ProfScope prof_(MOE_K_TC_F8, s);
-    return launch_pdl(use_pdl(p.rows), f8_tile_kernel<GATED>, dim3(int(std::min<int64_t>(units, num_sms()))),
+    return launch_pdl(use_pdl(p.rows), f8_tile_kernel<GATED, OUT>, dim3(int(std::min<int64_t>(units, num_sms()))),
                       dim3(THREADS), SMEM, s, A, B0, B1, p);
 }
 
@@ -435,7 +544,12 @@ cudaError_t launch_tile(const Args& p, bool gated, cudaStream_t s) {
     if (!map_bytes(&A, p.a, p.K, p.rows, 0, BM) || !map_bytes(&B0, p.b[0], p.K, p.N, p.E, box) ||
         !map_bytes(&B1, p.b[1], p.K, p.N, p.E, box))
         return cudaErrorInvalidValue;
-    return gated ? go<true>(A, B0, B1, p, s) : go<false>(A, B0, B1, p, s);
+    switch (p.out_dt) {
+        case MOE_DT_F32: return gated ? go<true, MOE_DT_F32>(A, B0, B1, p, s) : go<false, MOE_DT_F32>(A, B0, B1, p, s);
+        case MOE_DT_BF16: return gated ? go<true, MOE_DT_BF16>(A, B0, B1, p, s) : go<false, MOE_DT_BF16>(A, B0, B1, p, s);
+        case MOE_DT_F16: return gated ? go<true, MOE_DT_F16>(A, B0, B1, p, s) : go<false, MOE_DT_F16>(A, B0, B1, p, s);
+        default: return gated ? go<true, MOE_DT_E4M3>(A, B0, B1, p, s) : cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace f8

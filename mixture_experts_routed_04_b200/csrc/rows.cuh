@@ -9,6 +9,13 @@ namespace moe {
 
 MOE_DEV float f16_bits_to_f32(uint16_t v) { return f16_lo(uint32_t(v)); }
 
+// Two values to bf16, nearest even, in one instruction (NaN becomes the canonical NaN).
+MOE_DEV uint32_t cvt_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
 // One element of a row of dtype dt (MOE_DT_F32 / BF16 / F16).
 MOE_DEV float load_elem(const void* p, int64_t i, int dt) {
     if (dt == MOE_DT_F32) return static_cast<const float*>(p)[i];
@@ -17,12 +24,12 @@ MOE_DEV float load_elem(const void* p, int64_t i, int dt) {
 }
 MOE_DEV void store_elem(void* p, int64_t i, float v, int dt) {
     if (dt == MOE_DT_F32) static_cast<float*>(p)[i] = v;
-    else static_cast<uint16_t*>(p)[i] = uint16_t((dt == MOE_DT_BF16 ? f32_to_bf16_rne(v) : pack_f16x2(v, 0.f)) & 0xFFFFu);
+    else static_cast<uint16_t*>(p)[i] = uint16_t((dt == MOE_DT_BF16 ? cvt_bf16x2(v, 0.f) : pack_f16x2(v, 0.f)) & 0xFFFFu);
 }
 // v as the dtype holds it.
 MOE_DEV float round_to(float v, int dt) {
     if (dt == MOE_DT_F32) return v;
-    return dt == MOE_DT_BF16 ? __uint_as_float(f32_to_bf16_rne(v) << 16) : f16_lo(pack_f16x2(v, 0.f));
+    return dt == MOE_DT_BF16 ? bf16_lo(cvt_bf16x2(v, 0.f)) : f16_lo(pack_f16x2(v, 0.f));
 }
 
 MOE_DEV void unpack8(const uint4& r, bool bf16, float (&v)[8]) {
@@ -37,7 +44,7 @@ MOE_DEV uint4 pack8(const float (&v)[8], bool bf16) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        w[i] = bf16 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : pack_f16x2(v[2 * i], v[2 * i + 1]);
+        w[i] = bf16 ? cvt_bf16x2(v[2 * i], v[2 * i + 1]) : pack_f16x2(v[2 * i], v[2 * i + 1]);
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
