@@ -500,8 +500,8 @@ MOE_API int moe_expert_ffn_backward(const moe_params* p, const uint16_t* x, cons
  * Sums and statistics are fp32; each output is rounded once to its dtype.
  * Rows are [T, d] with their elements next to each other and ld_* elements from
  * row to row; any d up to MOE_NORM_MAX_D, any stride and any element-aligned
- * pointer is taken. Rows of a multiple of 8 elements that all start on 16 bytes
- * (every tensor of the call) are read in 16-byte vectors; others element by element.
+ * pointer is taken. Rows of a multiple of 4 elements that all start on 4 elements'
+ * bytes (every tensor of the call) are read 4 elements at a time; others one by one.
  * T = 0: nothing is launched; gradients summed over tokens are set to zero.
  */
 #define MOE_NORM_NONE  0
@@ -546,7 +546,7 @@ MOE_API size_t moe_norm_workspace_size(const moe_norm_params* p);
  * y      [T, d] block_dtype, or NULL when q8 is given; may be x itself (same dtype and stride)
  * q8, s8 NULL, or N(x) (before its rounding to block_dtype) as moe_quantize_f8 gives it:
  *        e4m3 [T, d] (row stride d) and its scales fp32 [ceil(d/128), T]. Needs d a multiple of 16
- *        and every tensor's rows on 16 bytes (MOE_ERR_INVALID_ARG / MOE_ERR_MISALIGNED)
+ *        and every tensor's rows on 4 elements' bytes (MOE_ERR_INVALID_ARG / MOE_ERR_MISALIGNED)
  * mean, rstd  fp32 [T] for the backward call, or NULL (mean is 0 for RMS)
  */
 MOE_API int moe_norm_forward(const moe_norm_params* p, const void* x, const void* weight, const void* bias, void* y,

@@ -179,9 +179,11 @@ def _p(t):
 
 
 def _stream(stream=None):
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: building the Stream object of torch.cuda.current_stream() takes longer than a launch
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def capacity(p: Params):
@@ -364,37 +366,40 @@ def prepare_down_f16(w_down, stream=None):
 # ------------------------------------------------------------------ norms around a block
 
 def _dt(t) -> int:
-    """The library's dtype code of a tensor."""
-    import torch
-    codes = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
-    if t.dtype not in codes:
-        raise MoeError(f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    """The library's dtype code of a tensor of 32 or 16 bits."""
+    return _dtypes("rows").index(t.dtype)  # MOE_DT_F32, _BF16, _F16
 
 
 def _fits(what, stream, *specs):
-    """Checks tensors against (name, tensor, shape, dtypes): on the device the call runs on, of the
-    shape and one of the dtypes, and contiguous where the shape is followed by True. None passes."""
+    """Checks tensors given as (name, tensor, shape, dtypes, dense): on the device the call runs on, of
+    the shape and one of the dtypes, contiguous where dense is true. None passes."""
     import torch
-    dev = stream.device if stream is not None else torch.device("cuda", torch.cuda.current_device())
-    if dev.index != torch.cuda.current_device():
+    dev = torch.cuda.current_device()
+    if stream is not None and stream.device_index != dev:
         raise MoeError(f"{what}: the stream is not on the current device")
     for name, t, shape, dtypes, dense in specs:
-        if t is None:
+        if t is None or (t.get_device() == dev and t.shape == shape and t.dtype in dtypes and
+                         (not dense or t.is_contiguous())):
             continue
-        if t.device != dev:
-            raise MoeError(f"{what}: {name} is on {t.device}, the call runs on {dev}")
-        if tuple(t.shape) != tuple(shape):
+        if t.get_device() != dev:
+            raise MoeError(f"{what}: {name} is on {t.device}, the call runs on cuda:{dev}")
+        if t.shape != shape:
             raise MoeError(f"{what}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-        if t.dtype not in dtypes:
-            raise MoeError(f"{what}: {name} is {t.dtype}")
-        if dense and not t.is_contiguous():
-            raise MoeError(f"{what}: {name} is not contiguous")
+        raise MoeError(f"{what}: {name} is {t.dtype}" if t.dtype not in dtypes else f"{what}: {name} is not contiguous")
+
+
+_dtype_table = None
 
 
 def _dtypes(code):
-    import torch
-    return ((torch.float32,), (torch.bfloat16,), (torch.float16,), (torch.float8_e4m3fn, torch.uint8))[code]
+    """The torch dtypes a dtype code stands for."""
+    global _dtype_table
+    if _dtype_table is None:
+        import torch
+        _dtype_table = {DT_F32: (torch.float32,), DT_BF16: (torch.bfloat16,), DT_F16: (torch.float16,),
+                        DT_E4M3: (torch.float8_e4m3fn, torch.uint8), "i32": (torch.int32,), "u8": (torch.uint8,),
+                        "rows": (torch.float32, torch.bfloat16, torch.float16)}
+    return _dtype_table[code]
 
 
 def norm_params(T, d, kind=NORM_RMS, next_kind=NORM_NONE, eps=1e-6, weight_offset=0.0, stream_dtype=DT_F32,
@@ -421,10 +426,12 @@ def _norm_grads(dw, db, dgate) -> NormGrads:
 
 def _rows_ok(what, p, ld, **tensors):
     """Row tensors: elements next to each other and the params' stride from row to row."""
+    ld = ld or p.d
     for name, t in tensors.items():
-        if t is not None and t.shape[0] > 0 and (t.stride(1) != 1 and t.shape[1] > 1 or
-                                                 t.shape[0] > 1 and t.stride(0) != (ld or p.d)):
-            raise MoeError(f"{what}: {name} has strides {t.stride()}, the params say {(ld or p.d, 1)}")
+        if t is None or t.is_contiguous() and ld == p.d:
+            continue
+        if t.shape[0] > 0 and (t.stride(1) != 1 and t.shape[1] > 1 or t.shape[0] > 1 and t.stride(0) != ld):
+            raise MoeError(f"{what}: {name} has strides {t.stride()}, the params say {(ld, 1)}")
 
 
 def norm_forward(p: NormParams, x, y, weight=None, bias=None, q8=None, s8=None, mean=None, rstd=None, stream=None):
@@ -518,13 +525,12 @@ def f8_workspace(p: F8Params, device="cuda"):
 def quantize_f8(x, q, s, ws, row_index=None, n_rows=None, stream=None):
     """moe_quantize_f8: rows of x (x[row_index] when given) to e4m3 q [rows, K] and scales s [ceil(K/128), rows].
     ws: 256 zeroed bytes (the error word); n_rows: device int32, rows from it on are left as they were."""
-    import torch
     rows, K = q.shape
-    _fits("moe_quantize_f8", stream, ("x", x, (x.shape[0], K), (torch.float32, torch.bfloat16, torch.float16), False),
-          ("q", q, (rows, K), _dtypes(DT_E4M3), True), ("s", s, ((K + 127) // 128, rows), (torch.float32,), True),
-          ("row_index", row_index, (rows,), (torch.int32,), True),
-          ("n_rows", n_rows, () if n_rows is None else n_rows.shape, (torch.int32,), True),
-          ("ws", ws, ws.shape, (torch.uint8,), True))
+    _fits("moe_quantize_f8", stream, ("x", x, (x.shape[0], K), _dtypes("rows"), False),
+          ("q", q, (rows, K), _dtypes(DT_E4M3), True), ("s", s, ((K + 127) // 128, rows), _dtypes(DT_F32), True),
+          ("row_index", row_index, (rows,), _dtypes("i32"), True),
+          ("n_rows", n_rows, () if n_rows is None else n_rows.shape, _dtypes("i32"), True),
+          ("ws", ws, ws.shape, _dtypes("u8"), True))
     if x.shape[0] > 0 and (K > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < K):
         raise MoeError(f"moe_quantize_f8: x has strides {x.stride()}")
     check(lib().moe_quantize_f8(rows, K, _p(x), _dt(x), x.stride(0) if x.shape[0] > 1 else K, x.shape[0],
@@ -534,45 +540,39 @@ def quantize_f8(x, q, s, ws, row_index=None, n_rows=None, stream=None):
 
 def quantize_f8_weights(w, q, s, transposed=False, stream=None):
     """moe_quantize_f8_weights: w [E, N, K] ([E, K, N] with transposed) to e4m3 q [E, N, K] and its block scales."""
-    import torch
     E, N, K = q.shape
-    _fits("moe_quantize_f8_weights", stream,
-          ("w", w, (E, K, N) if transposed else (E, N, K), (torch.float32, torch.bfloat16, torch.float16), True),
+    _fits("moe_quantize_f8_weights", stream, ("w", w, (E, K, N) if transposed else (E, N, K), _dtypes("rows"), True),
           ("q", q, (E, N, K), _dtypes(DT_E4M3), True),
-          ("s", s, (E, (N + 127) // 128, (K + 127) // 128), (torch.float32,), True))
+          ("s", s, (E, (N + 127) // 128, (K + 127) // 128), _dtypes(DT_F32), True))
     check(lib().moe_quantize_f8_weights(E, N, K, _p(w), _dt(w), int(bool(transposed)), _p(q), _p(s),
                                         _stream(stream)), "moe_quantize_f8_weights")
 
 
-def _f8_operands(what, stream, p, a, a_scale, offsets, ws, *more):
-    import torch
-    f8, f32 = _dtypes(DT_E4M3), (torch.float32,)
+def _f8_specs(p, a, a_scale, offsets, ws, *weights):
+    """What _fits checks of the operands every product takes; weights: (name, tensor, scales)."""
+    f8, f32, i32, u8 = _dtypes(DT_E4M3), _dtypes(DT_F32), _dtypes("i32"), _dtypes("u8")
     kb, nb = (p.K + 127) // 128, (p.N + 127) // 128
-    named = []
-    for name, t in more:
-        named.append((name, t, (p.E, p.N, p.K), f8, True) if not name.startswith("scale of ") else
-                     (name, t, (p.E, nb, kb), f32, True))
-    _fits(what, stream, ("a", a, (p.rows, p.K), f8, True), ("a_scale", a_scale, (kb, p.rows), f32, True),
-          ("offsets", offsets, (p.E + 1,), (torch.int32,), True), ("ws", ws, ws.shape, (torch.uint8,), True), *named)
+    specs = [("a", a, (p.rows, p.K), f8, True), ("a_scale", a_scale, (kb, p.rows), f32, True),
+             ("offsets", offsets, (p.E + 1,), i32, True), ("ws", ws, ws.shape, u8, True)]
+    for name, t, s in weights:
+        specs += [(name, t, (p.E, p.N, p.K), f8, True), ("the scales of " + name, s, (p.E, nb, kb), f32, True)]
+    return specs
 
 
 def matmul_f8(p: F8Params, a, a_scale, b, b_scale, out, ws, offsets=None, sorted_pair=None, topk_w=None, stream=None):
     """moe_matmul_f8: out = w_r * a b^T by expert, e4m3 with scales for each block of 128."""
-    import torch
-    _f8_operands("moe_matmul_f8", stream, p, a, a_scale, offsets, ws, ("b", b), ("scale of b", b_scale))
-    _fits("moe_matmul_f8", stream, ("out", out, (p.rows, p.N), _dtypes(p.out_dtype), True),
-          ("sorted_pair", sorted_pair, (p.rows,), (torch.int32,), True),
-          ("topk_w", topk_w, () if topk_w is None else topk_w.shape, (torch.float32,), True))
+    _fits("moe_matmul_f8", stream, *_f8_specs(p, a, a_scale, offsets, ws, ("b", b, b_scale)),
+          ("out", out, (p.rows, p.N), _dtypes(p.out_dtype), True),
+          ("sorted_pair", sorted_pair, (p.rows,), _dtypes("i32"), True),
+          ("topk_w", topk_w, () if topk_w is None else topk_w.shape, _dtypes(DT_F32), True))
     check(lib().moe_matmul_f8(ctypes.byref(p), _p(a), _p(a_scale), _p(offsets), _p(b), _p(b_scale), _p(sorted_pair),
                               _p(topk_w), _p(out), _p(ws), ws.numel(), _stream(stream)), "moe_matmul_f8")
 
 
 def gated_f8(p: F8Params, a, a_scale, w_gate, s_gate, w_up, s_up, h, ws, h_scale=None, offsets=None, stream=None):
     """moe_gated_f8: h = silu(clamp(a w_gate^T)) * clamp(a w_up^T) by expert; e4m3 h with h_scale."""
-    import torch
-    _f8_operands("moe_gated_f8", stream, p, a, a_scale, offsets, ws, ("w_gate", w_gate), ("scale of w_gate", s_gate),
-                 ("w_up", w_up), ("scale of w_up", s_up))
-    _fits("moe_gated_f8", stream, ("h", h, (p.rows, p.N), _dtypes(p.out_dtype), True),
-          ("h_scale", h_scale, ((p.N + 127) // 128, p.rows), (torch.float32,), True))
+    _fits("moe_gated_f8", stream, *_f8_specs(p, a, a_scale, offsets, ws, ("w_gate", w_gate, s_gate), ("w_up", w_up, s_up)),
+          ("h", h, (p.rows, p.N), _dtypes(p.out_dtype), True),
+          ("h_scale", h_scale, ((p.N + 127) // 128, p.rows), _dtypes(DT_F32), True))
     check(lib().moe_gated_f8(ctypes.byref(p), _p(a), _p(a_scale), _p(offsets), _p(w_gate), _p(s_gate), _p(w_up),
                              _p(s_up), _p(h), _p(h_scale), _p(ws), ws.numel(), _stream(stream)), "moe_gated_f8")

@@ -24,6 +24,7 @@
 // Units (expert, n-tile, M-tile; M fastest, so that neighbours share the weights in
 // L2) are all alike in length and dealt out by index: no counter, no workspace.
 #include <algorithm>
+#include <atomic>
 
 #include "f8.cuh"
 #include "tmap.h"
@@ -400,28 +401,28 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t tb = tmem_base + lanes + uint32_t(acc * BN);
-                // the next 16 columns are on their way while these are added; the accumulator
-                // is handed back as soon as the last have come
-                uint32_t t[2][16];
-                auto col_of = [&](int c) { return c < CW / 32 ? c0 + c * 16 : c1 + (c - CW / 32) * 16; };
-                ld16(tb + col_of(0), t[0]);
+                // 64 columns at a time: one latency for four loads; the accumulator is handed back
+                // as soon as the last have come
 #pragma unroll
-                for (int c = 0; c < CW / 16; ++c) {
-                    wait16(t[c & 1]);
-                    if (c < CW / 16 - 1) {
-                        ld16(tb + col_of(c + 1), t[(c + 1) & 1]);
-                    } else {
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t t[2][32];
+                    const uint32_t ch = tb + (h ? c1 : c0);
+                    tmem_ld_32x32b_x32(ch, t[0]);
+                    tmem_ld_32x32b_x32(ch + 32, t[1]);
+                    tmem_ld_wait(t[0]);
+                    tmem_ld_wait(t[1]);
+                    if (h == 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(ms->tempty + acc);
                     }
-                    const float f = c < CW / 32 ? f0 : f1;
+                    const float f = h ? f1 : f0;
                     const float2 ff = make_float2(f, f);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        s[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(t[c & 1][2 * i]),
-                                                              __uint_as_float(t[c & 1][2 * i + 1])),
-                                                  ff, s[c * 8 + i]);
+                    for (int i = 0; i < 32; ++i)
+                        s[h * 32 + i] = __ffma2_rn(make_float2(__uint_as_float(t[i >> 4][2 * (i & 15)]),
+                                                               __uint_as_float(t[i >> 4][2 * (i & 15) + 1])),
+                                                   ff, s[h * 32 + i]);
                 }
                 if (++acc == 2) {
                     acc = 0;
@@ -519,8 +520,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 template <bool GATED, int OUT>
 cudaError_t go(const CUtensorMap& A, const CUtensorMap& B0, const CUtensorMap& B1, const Args& p, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(f8_tile_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> configured{0};  // one bit a device
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev >= 64 || !(configured.load() & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(f8_tile_kernel<GATED, OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
     const int64_t mt = p.offsets ? std::min<int64_t>(p.rows, p.E) + p.rows / BM : (p.rows + BM - 1) / BM;
     const int64_t units = mt * ((p.N + (GATED ? 127 : BN - 1)) / (GATED ? 128 : BN));
     ProfScope prof_(MOE_K_TC_F8, s);

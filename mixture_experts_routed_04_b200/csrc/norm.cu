@@ -22,6 +22,8 @@
 // a second kernel adds the groups' sums in a fixed order, so that a call's result
 // does not change from run to run (no atomics).
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -30,6 +32,12 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+
+// How a row gets into registers: element by element (any alignment), by 16-byte loads (few rows,
+// where the way is shortest), or by 16-byte asynchronous copies of the next rows into shared memory
+// (many rows: HBM stays busy while a row is summed). kStagedFull: rows of exactly 8 * NV * 32 W.
+enum Mode { kScalar = 0, kVec = 1, kStaged = 2, kStagedFull = 3 };
+__host__ __device__ constexpr int layout_of(int mode) { return mode == kScalar ? kScalarRow : mode == kStagedFull ? kFullRow : kVecRow; }
 
 struct NormArgs {
     const void* x;       // pre: x (stream dtype); post: the block's output (block dtype)
@@ -52,23 +60,38 @@ struct NormArgs {
     float eps, offset, alpha, beta;
 };
 
-// Sum of a value over the wpr warps of a row; every thread of the block calls it.
-MOE_DEV float row_sum(float v, int wpr, float* buf) {
+// Sums of N values over the W warps of a row, together; every thread of the block calls it.
+// buf: 8 floats a value.
+template <int W, int N>
+MOE_DEV void row_sums(float (&v)[N], float* buf) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (wpr == 1) return v;
-    const int warp = threadIdx.x >> 5, g0 = warp / wpr * wpr;
-    if ((threadIdx.x & 31) == 0) buf[warp] = v;
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xFFFFFFFFu, v[n], o);
+    if (W == 1) return;
+    const int warp = threadIdx.x >> 5, g0 = warp / W * W;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) buf[n * 8 + warp] = v[n];
+    }
     __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < wpr; ++i) s += buf[g0 + i];
-    return s;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        v[n] = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[n] += buf[n * 8 + g0 + i];
+    }
+}
+template <int W>
+MOE_DEV float row_sum(float v, float* buf) {
+    float a[1] = {v};
+    row_sums<W>(a, buf);
+    return a[0];
 }
 
-// Mean and 1/sqrt(var + eps) of the row in v; buf: 16 floats of the block.
-template <int NV, bool VEC>
-MOE_DEV void row_stats(const float (&v)[NV][8], int kind, int d, float eps, int wpr, int th, int t, float* buf,
-                       float& mean, float& rstd) {
+// Mean and 1/sqrt(var + eps) of the row in v, which becomes v - mean; buf: 16 floats of the block.
+template <int W, int NV, int L>
+MOE_DEV void row_stats(float (&v)[NV][8], int kind, int d, float eps, int t, float* buf, float& mean, float& rstd) {
     mean = 0.f;
     if (kind == MOE_NORM_LAYER) {
         float s = 0.f;
@@ -76,41 +99,54 @@ MOE_DEV void row_stats(const float (&v)[NV][8], int kind, int d, float eps, int 
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s += v[i][j];
-        mean = row_sum(s, wpr, buf) / float(d);
+        mean = row_sum<W>(s, buf) / float(d);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = in_row<L>(i, j, d, 32 * W, t) ? v[i][j] - mean : 0.f;
     }
-    float s = 0.f;
+    float s = 0.f;  // elements past the row are zero
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float c = in_row<VEC>(i, j, d, th, t) ? v[i][j] - mean : 0.f;
-            s = fmaf(c, c, s);
-        }
-    rstd = 1.0f / sqrtf(row_sum(s, wpr, buf + 8) / float(d) + eps);
+        for (int j = 0; j < 8; ++j) s = fmaf(v[i][j], v[i][j], s);
+    rstd = 1.0f / sqrtf(row_sum<W>(s, buf + 8) / float(d) + eps);
 }
 
-// v <- (v - mean) rstd (w + o) + b
-template <int NV, bool VEC>
-MOE_DEV void apply_norm(float (&v)[NV][8], float mean, float rstd, const void* w, const void* b, float offset,
-                        int param_dt, int d, int th, int t) {
-    float p[NV][8];
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = (v[i][j] - mean) * rstd;
+// v <- v rstd (w + o) + b; the weights, from L1 after the first rows, 8 at a time
+template <int W, int NV, int L>
+MOE_DEV void apply_norm(float (&v)[NV][8], float rstd, const void* w, const void* b, float offset, int param_dt, int d,
+                        int t) {
     if (w) {
-        load_row<NV, VEC>(p, w, d, param_dt, th, t);
+        by_dtype(param_dt, [&](auto DT) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float p[8];
+                load_group<L, decltype(DT)::value>(p, w, i, d, 32 * W, t);
+                if (offset != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) p[j] += offset;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * p[j];
+            }
+        });
+    } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= p[i][j] + offset;
+            for (int j = 0; j < 8; ++j) v[i][j] *= rstd;
     }
     if (b) {
-        load_row<NV, VEC>(p, b, d, param_dt, th, t);
+        by_dtype(param_dt, [&](auto DT) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                float p[8];
+                load_group<L, decltype(DT)::value>(p, b, i, d, 32 * W, t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] += p[i][j];
+                for (int j = 0; j < 8; ++j) v[i][j] += p[j];
+            }
+        });
     }
 }
 
@@ -118,64 +154,100 @@ MOE_DEV char* at_row(const void* p, int64_t row, int64_t ld, int dt) {
     return static_cast<char*>(const_cast<void*>(p)) + row * ld * (dt == MOE_DT_F32 ? 4 : 2);
 }
 
-template <int NV, bool VEC, bool POST>
-__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const NormArgs a, int wpr) {
+template <int W, int NV, int MODE, bool POST>
+__global__ void __launch_bounds__(kThreads, 2) norm_forward_kernel(const NormArgs a, const int depth) {
+    constexpr int L = layout_of(MODE);
+    constexpr bool STAGED = MODE >= kStaged;
+    extern __shared__ uint4 stage[];  // STAGED: depth rows of every tensor
     __shared__ float buf[2][16];
     griddep_wait();
     griddep_launch();
-    const int th = wpr * 32, t = threadIdx.x % th, rpb = kThreads / th;
+    constexpr int th = 32 * W, rpb = kThreads / th;
+    const int t = threadIdx.x % th;
     const int d = a.d;
-    for (int64_t r0 = int64_t(blockIdx.x) * rpb; r0 < a.T; r0 += int64_t(gridDim.x) * rpb) {
+    const int x_dt = POST ? a.block_dt : a.stream_dt;
+    const int64_t ld_x = POST ? a.ld_block : a.ld_stream, step = int64_t(gridDim.x) * rpb;
+    const int px = stage_pieces(NV, x_dt), pieces = px + (POST ? stage_pieces(NV, a.stream_dt) : 0);
+    auto fetch = [&](int slot, int64_t r) {  // the row's copies, in a group of their own
+        if (r < a.T) {
+            const uint32_t dst = smem_u32(stage + slot * pieces * kThreads);
+            copy_row<NV, L, kThreads>(dst, at_row(a.x, r, ld_x, x_dt), d, x_dt, th, t);
+            if (POST)
+                copy_row<NV, L, kThreads>(dst + px * kThreads * 16, at_row(a.resid, r, a.ld_stream, a.stream_dt), d,
+                             a.stream_dt, th, t);
+        }
+        cp_async_commit();
+    };
+    const int64_t first = int64_t(blockIdx.x) * rpb + threadIdx.x / th;
+    int slot = 0;
+    if (STAGED)
+        for (int i = 0; i < depth; ++i) fetch(i, first + i * step);
+    for (int64_t r0 = int64_t(blockIdx.x) * rpb; r0 < a.T; r0 += step) {
         // rows past T take part in the block's reductions and store nothing
         const int64_t r = r0 + threadIdx.x / th;
         const bool live = r < a.T;
         const int dl = live ? d : 0;
         float v[NV][8];
-        load_row<NV, VEC>(v, at_row(a.x, live ? r : 0, POST ? a.ld_block : a.ld_stream, POST ? a.block_dt : a.stream_dt),
-                          dl, POST ? a.block_dt : a.stream_dt, th, t);
         float res[POST ? NV : 1][8];
-        if constexpr (POST)
-            load_row<NV, VEC>(res, at_row(a.resid, live ? r : 0, a.ld_stream, a.stream_dt), dl, a.stream_dt, th, t);
+        if constexpr (STAGED) {
+            cp_async_wait_most(depth - 1);
+            const uint4* src = stage + slot * pieces * kThreads;
+            read_row<NV, L, kThreads>(v, src, dl, x_dt, th, t);
+            if constexpr (POST) read_row<NV, L, kThreads>(res, src + px * kThreads, dl, a.stream_dt, th, t);
+        } else {
+            load_row<NV, L>(v, at_row(a.x, live ? r : 0, ld_x, x_dt), dl, x_dt, th, t);
+            if constexpr (POST)
+                load_row<NV, L>(res, at_row(a.resid, live ? r : 0, a.ld_stream, a.stream_dt), dl, a.stream_dt, th, t);
+        }
         if (a.kind != MOE_NORM_NONE) {
             float mean, rstd;
-            row_stats<NV, VEC>(v, a.kind, d, a.eps, wpr, th, t, buf[0], mean, rstd);
+            row_stats<W, NV, L>(v, a.kind, d, a.eps, t, buf[0], mean, rstd);
             if (live && t == 0) {
                 if (a.mean) a.mean[r] = mean;
                 if (a.rstd) a.rstd[r] = rstd;
             }
-            apply_norm<NV, VEC>(v, mean, rstd, a.weight, a.bias, a.offset, a.param_dt, d, th, t);
+            apply_norm<W, NV, L>(v, rstd, a.weight, a.bias, a.offset, a.param_dt, d, t);
         }
         if constexpr (POST) {
             float gt = a.beta;
             if (a.gate_kind == MOE_GATE_TOKEN) gt *= live ? load_elem(a.gate, r, a.param_dt) : 0.f;
             if (a.gate_kind == MOE_GATE_CHANNEL) {
-                float p[NV][8];
-                load_row<NV, VEC>(p, a.gate, d, a.param_dt, th, t);
+                by_dtype(a.param_dt, [&](auto DT) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        float p[8];
+                        load_group<L, decltype(DT)::value>(p, a.gate, i, d, th, t);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) v[i][j] *= p[j];
+                    }
+                });
+            }
+            by_dtype(a.stream_dt, [&](auto DT) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[i][j] *= p[i][j];
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = round_to(fmaf(a.alpha, res[i][j], gt * v[i][j]), a.stream_dt);
-            if (live) store_row<NV, VEC>(v, at_row(a.out, r, a.ld_stream, a.stream_dt), d, a.stream_dt, th, t);
+                    for (int j = 0; j < 8; ++j) v[i][j] = round_to(fmaf(a.alpha, res[i][j], gt * v[i][j]), decltype(DT)::value);
+            });
+            if (live) store_row<NV, L>(v, at_row(a.out, r, a.ld_stream, a.stream_dt), d, a.stream_dt, th, t);
             if (a.next_kind != MOE_NORM_NONE) {
                 float mean, rstd;
-                row_stats<NV, VEC>(v, a.next_kind, d, a.eps, wpr, th, t, buf[1], mean, rstd);
+                row_stats<W, NV, L>(v, a.next_kind, d, a.eps, t, buf[1], mean, rstd);
                 if (live && t == 0) {
                     if (a.next_mean) a.next_mean[r] = mean;
                     if (a.next_rstd) a.next_rstd[r] = rstd;
                 }
-                apply_norm<NV, VEC>(v, mean, rstd, a.next_weight, a.next_bias, a.offset, a.param_dt, d, th, t);
+                apply_norm<W, NV, L>(v, rstd, a.next_weight, a.next_bias, a.offset, a.param_dt, d, t);
             }
         }
-        if (a.y && live) store_row<NV, VEC>(v, at_row(a.y, r, a.ld_block, a.block_dt), d, a.block_dt, th, t);
-        if constexpr (VEC) {
-            if (a.q8) store_row_e4m3<NV>(v, a.q8 + (live ? r : 0) * d, a.s8 + (live ? r : 0), a.T, dl, th, t);
+        if (a.y && live) store_row<NV, L>(v, at_row(a.y, r, a.ld_block, a.block_dt), d, a.block_dt, th, t);
+        if constexpr (L != kScalarRow) {
+            if (a.q8) store_row_e4m3<NV, L == kScalarRow ? kVecRow : L>(v, a.q8 + (live ? r : 0) * d, a.s8 + (live ? r : 0), a.T, dl, th, t);
         }
-        if (wpr > 1) __syncthreads();  // the block's sums are read before the next rows write theirs
+        if constexpr (STAGED) {  // the row is in registers: its place takes the row `depth` on
+            fetch(slot, r + depth * step);
+            slot = slot + 1 == depth ? 0 : slot + 1;
+        }
+        if (W > 1) __syncthreads();  // the block's sums are read before the next rows write theirs
     }
 }
 
@@ -191,33 +263,75 @@ struct NormBwdArgs {
     void* dx;           // as x
     void* dresid;       // post: alpha dout (stream dtype), or null
     float* dgate_tok;   // post, gate per token: [T], or null
-    float* s1;          // [groups, d] sums of rs D xhat, or null
-    float* s0;          // [groups, d] sums of rs D, or null
+    float* s1;          // [blocks, d] sums of rs D xhat, or null: no sums over tokens
+    float* s0;          // [blocks, d] sums of rs D (S0)
     int64_t ld_x, ld_dy;
     int T, d, kind, x_dt, dy_dt, param_dt, gate_kind;
     float offset, alpha, beta;
 };
 
-template <int NV, bool VEC, bool POST>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwdArgs a, int wpr) {
+// Backward blocks an SM (their registers): also the grid, whose partial sums are written and read once
+// more, so few enough that they stay small beside the rows.
+__host__ __device__ constexpr int bwd_blocks(int nv, bool s0) { return nv <= 2 && !s0 ? 3 : 2; }
+constexpr int kBwdBlocksMost = 3;
+
+// S0: whether sums without xhat are wanted (a bias).
+template <int W, int NV, int MODE, bool POST, bool S0>
+__global__ void __launch_bounds__(kThreads, bwd_blocks(NV, S0)) norm_backward_kernel(const NormBwdArgs a, const int depth) {
+    constexpr int L = layout_of(MODE);
+    constexpr bool STAGED = MODE >= kStaged;
+    constexpr int th = 32 * W, rpb = kThreads / th;
     __shared__ float buf[24];
+    extern __shared__ uint4 stage[];  // STAGED: depth rows of every tensor; at the end, rpb > 1: sums [1 + S0][d]
+    float* sums = reinterpret_cast<float*>(stage);
     griddep_wait();
-    griddep_launch();
-    const int th = wpr * 32, t = threadIdx.x % th, rpb = kThreads / th;
+    const int t = threadIdx.x % th;
     const int d = a.d;
     const float inv_d = 1.0f / float(d);
-    float s1[NV][8], s0[NV][8];
+    float s1[NV][8], s0[S0 ? NV : 1][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s1[i][j] = s0[i][j] = 0.f;
-    for (int64_t r0 = int64_t(blockIdx.x) * rpb; r0 < a.T; r0 += int64_t(gridDim.x) * rpb) {
+        for (int j = 0; j < 8; ++j) {
+            s1[i][j] = 0.f;
+            if (S0) s0[i][j] = 0.f;
+        }
+    const int64_t step = int64_t(gridDim.x) * rpb;
+    const int px = stage_pieces(NV, a.x_dt), pg = px + stage_pieces(NV, a.dy_dt), pieces = pg + (!POST && a.dres ? px : 0);
+    auto fetch = [&](int slot, int64_t r) {
+        if (r < a.T) {
+            const uint32_t dst = smem_u32(stage + slot * pieces * kThreads);
+            copy_row<NV, L, kThreads>(dst, at_row(a.x, r, a.ld_x, a.x_dt), d, a.x_dt, th, t);
+            copy_row<NV, L, kThreads>(dst + px * kThreads * 16, at_row(a.dy, r, a.ld_dy, a.dy_dt), d, a.dy_dt, th, t);
+            if (!POST && a.dres)
+                copy_row<NV, L, kThreads>(dst + pg * kThreads * 16, at_row(a.dres, r, a.ld_x, a.x_dt), d, a.x_dt, th, t);
+        }
+        cp_async_commit();
+    };
+    const int64_t first = int64_t(blockIdx.x) * rpb + threadIdx.x / th;
+    int slot = 0;
+    if (STAGED)
+        for (int i = 0; i < depth; ++i) fetch(i, first + i * step);
+    for (int64_t r0 = int64_t(blockIdx.x) * rpb; r0 < a.T; r0 += step) {
         const int64_t r = r0 + threadIdx.x / th;
         const bool live = r < a.T;
         const int dl = live ? d : 0;
-        float x[NV][8], g[NV][8], p[NV][8];
-        load_row<NV, VEC>(x, at_row(a.x, live ? r : 0, a.ld_x, a.x_dt), dl, a.x_dt, th, t);
-        load_row<NV, VEC>(g, at_row(a.dy, live ? r : 0, a.ld_dy, a.dy_dt), dl, a.dy_dt, th, t);
+        float x[NV][8], g[NV][8];
+        const uint4* src = stage + slot * pieces * kThreads;
+        if constexpr (STAGED) {
+            cp_async_wait_most(depth - 1);
+            read_row<NV, L, kThreads>(x, src, dl, a.x_dt, th, t);
+            read_row<NV, L, kThreads>(g, src + px * kThreads, dl, a.dy_dt, th, t);
+            if (L == kFullRow && !live) {  // nothing was copied for a row past T
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[i][j] = g[i][j] = 0.f;
+            }
+        } else {
+            load_row<NV, L>(x, at_row(a.x, live ? r : 0, a.ld_x, a.x_dt), dl, a.x_dt, th, t);
+            load_row<NV, L>(g, at_row(a.dy, live ? r : 0, a.ld_dy, a.dy_dt), dl, a.dy_dt, th, t);
+        }
         const float mean = live && a.kind == MOE_NORM_LAYER ? a.mean[r] : 0.f;
         const float rstd = live && a.kind != MOE_NORM_NONE ? a.rstd[r] : 1.f;
         float rs = 1.f;
@@ -230,68 +344,55 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwdAr
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) q[i][j] = a.alpha * g[i][j];
-                store_row<NV, VEC>(q, at_row(a.dresid, r, a.ld_dy, a.dy_dt), d, a.dy_dt, th, t);
+                store_row<NV, L>(q, at_row(a.dresid, r, a.ld_dy, a.dy_dt), d, a.dy_dt, th, t);
             }
         }
+        // g becomes the gradient of xhat without the row's factor rs; on the way the sums over
+        // tokens (s1, s0), the row's two sums and a token gate's gradient
+        float dot_n = 0.f, sa = 0.f, sb = 0.f;
+        by_dtype(a.param_dt, [&](auto DT) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+            for (int i = 0; i < NV; ++i) {
+                float p[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[i][j] = in_row<VEC>(i, j, dl, th, t) ? (x[i][j] - mean) * rstd : 0.f;
-                s1[i][j] = fmaf(rs * g[i][j], x[i][j], s1[i][j]);
-                s0[i][j] = fmaf(rs, g[i][j], s0[i][j]);
-            }
-        // g <- the gradient of xhat without the row's factor rs; the token gate's gradient on the way
-        float dot_n = 0.f;
-        if (a.weight) {
-            load_row<NV, VEC>(p, a.weight, d, a.param_dt, th, t);
+                for (int j = 0; j < 8; ++j) {
+                    x[i][j] = (x[i][j] - mean) * rstd;  // past the row: any number, its g is zero
+                    const float e = rs * g[i][j];
+                    s1[i][j] = fmaf(e, x[i][j], s1[i][j]);
+                    if (S0) s0[i][j] += e;
+                }
+                if (POST && a.dgate_tok && a.bias) {
+                    load_group<L, decltype(DT)::value>(p, a.bias, i, d, th, t);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                    for (int j = 0; j < 8; ++j) dot_n = fmaf(g[i][j], p[j], dot_n);
+                }
+                if (a.weight) {
+                    load_group<L, decltype(DT)::value>(p, a.weight, i, d, th, t);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) p[i][j] = in_row<VEC>(i, j, d, th, t) ? p[i][j] + a.offset : 0.f;
-        }
-        if (POST && a.dgate_tok) {
-            if (a.bias) {
-                float q[NV][8];
-                load_row<NV, VEC>(q, a.bias, d, a.param_dt, th, t);
+                    for (int j = 0; j < 8; ++j) g[i][j] *= p[j] + a.offset;
+                }
+                if (POST && a.dgate_tok) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
+                    for (int j = 0; j < 8; ++j) dot_n = fmaf(g[i][j], x[i][j], dot_n);
+                }
+                if (POST && a.gate_kind == MOE_GATE_CHANNEL) {
+                    load_group<L, decltype(DT)::value>(p, a.gate, i, d, th, t);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) dot_n = fmaf(g[i][j], q[i][j], dot_n);
-            }
-        }
-        if (a.weight) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[i][j] *= p[i][j];
-        }
-        if (POST && a.dgate_tok) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) dot_n = fmaf(g[i][j], x[i][j], dot_n);
-            dot_n = row_sum(dot_n, wpr, buf + 16);
-            if (live && t == 0) a.dgate_tok[r] = a.beta * dot_n;
-        }
-        if (POST && a.gate_kind == MOE_GATE_CHANNEL) {
-            load_row<NV, VEC>(p, a.gate, d, a.param_dt, th, t);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) g[i][j] *= p[i][j];
-        }
-        if (a.kind != MOE_NORM_NONE) {
-            float sa = 0.f, sb = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
+                    for (int j = 0; j < 8; ++j) g[i][j] *= p[j];
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     sa = fmaf(g[i][j], x[i][j], sa);
                     sb += g[i][j];
                 }
-            sa = row_sum(sa, wpr, buf) * inv_d;
-            sb = a.kind == MOE_NORM_LAYER ? row_sum(sb, wpr, buf + 8) * inv_d : 0.f;
+            }
+        });
+        float sums3[3] = {sa, sb, dot_n};
+        row_sums<W>(sums3, buf);
+        if (POST && a.dgate_tok && live && t == 0) a.dgate_tok[r] = a.beta * sums3[2];
+        if (a.kind != MOE_NORM_NONE) {
+            sa = sums3[0] * inv_d;
+            sb = a.kind == MOE_NORM_LAYER ? sums3[1] * inv_d : 0.f;
             const float f = rs * rstd;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -304,23 +405,60 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const NormBwdAr
                 for (int j = 0; j < 8; ++j) g[i][j] *= rs;
         }
         if (!POST && a.dres) {
-            load_row<NV, VEC>(p, at_row(a.dres, live ? r : 0, a.ld_x, a.x_dt), dl, a.x_dt, th, t);
+            if constexpr (STAGED) read_row<NV, L, kThreads>(x, src + pg * kThreads, dl, a.x_dt, th, t);
+            else load_row<NV, L>(x, at_row(a.dres, live ? r : 0, a.ld_x, a.x_dt), dl, a.x_dt, th, t);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[i][j] += p[i][j];
+                for (int j = 0; j < 8; ++j) g[i][j] += x[i][j];
         }
-        if (live) store_row<NV, VEC>(g, at_row(a.dx, r, a.ld_x, a.x_dt), d, a.x_dt, th, t);
-        if (wpr > 1) __syncthreads();
+        if (live) store_row<NV, L>(g, at_row(a.dx, r, a.ld_x, a.x_dt), d, a.x_dt, th, t);
+        if constexpr (STAGED) {
+            fetch(slot, r + depth * step);
+            slot = slot + 1 == depth ? 0 : slot + 1;
+        }
+        if (W > 1) __syncthreads();
     }
-    const int64_t grp = int64_t(blockIdx.x) * rpb + threadIdx.x / th;
-    if (a.s1) store_row<NV, VEC>(s1, a.s1 + grp * d, d, MOE_DT_F32, th, t);
-    if (a.s0) store_row<NV, VEC>(s0, a.s0 + grp * d, d, MOE_DT_F32, th, t);
+    if constexpr (STAGED) {
+        cp_async_wait<0>();  // (groups without copies)
+        __syncthreads();     // the stages become the sums' place
+    }
+    griddep_launch();
+    if (!a.s1) return;
+    // the block's rows added in the order of its groups of warps, then one row of sums a block
+    if (rpb > 1) {
+        const int grp = threadIdx.x / th;
+        for (int k = 1; k < rpb; ++k) {
+            if (grp == k) {
+                store_row<NV, L>(s1, sums, d, MOE_DT_F32, th, t);
+                if constexpr (S0) store_row<NV, L>(s0, sums + d, d, MOE_DT_F32, th, t);
+            }
+            __syncthreads();
+            if (grp == 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    float p[8];
+                    load_group<L, MOE_DT_F32>(p, sums, i, d, th, t);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) s1[i][j] += p[j];
+                    if constexpr (S0) {
+                        load_group<L, MOE_DT_F32>(p, sums + d, i, d, th, t);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) s0[i][j] += p[j];
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (grp != 0) return;
+    }
+    store_row<NV, L>(s1, a.s1 + int64_t(blockIdx.x) * d, d, MOE_DT_F32, th, t);
+    if constexpr (S0) store_row<NV, L>(s0, a.s0 + int64_t(blockIdx.x) * d, d, MOE_DT_F32, th, t);
 }
 
-// The groups' partial sums added in order: block of 32 columns x 32 strips of groups,
-// then the strips. dw = gate S1, db = gate S0, dgate = (w + o) S1 + b S0 (gate per
-// channel; else gate = 1 here, the token's gate and beta being in the sums).
+// The blocks' partial sums added in a fixed order: 8 columns x 128 strips of blocks, then the
+// strips. dw = gate S1, db = gate S0, dgate = (w + o) S1 + b S0 (gate per channel; else gate = 1
+// here, the token's gate and beta being in the sums).
 struct NormSumArgs {
     const float* s1;
     const float* s0;
@@ -330,36 +468,45 @@ struct NormSumArgs {
     float* dw;
     float* db;
     float* dgate;
-    int groups, d, param_dt;
+    int blocks, d, param_dt;
     float offset;
 };
 
-__global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs a) {
-    __shared__ float sm[2][32][33];
+constexpr int kSumCols = 8, kSumStrips = 128;
+
+__global__ void __launch_bounds__(kSumCols* kSumStrips) norm_sum_kernel(const NormSumArgs a) {
+    __shared__ float sm[2][kSumStrips][kSumCols + 1];
     griddep_wait();
     griddep_launch();
-    const int cx = threadIdx.x & 31, sy = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + cx;
+    const int cx = threadIdx.x % kSumCols, sy = threadIdx.x / kSumCols;
+    const int c = blockIdx.x * kSumCols + cx;
     float v1 = 0.f, v0 = 0.f;
     if (c < a.d) {
 #pragma unroll 4
-        for (int g = sy; g < a.groups; g += 32) {
-            if (a.s1) v1 += a.s1[int64_t(g) * a.d + c];
+        for (int g = sy; g < a.blocks; g += kSumStrips) {
+            v1 += a.s1[int64_t(g) * a.d + c];
             if (a.s0) v0 += a.s0[int64_t(g) * a.d + c];
         }
     }
     sm[0][sy][cx] = v1;
     sm[1][sy][cx] = v0;
     __syncthreads();
-    // warp y adds the 32 strips of column y
-    float w1 = sm[0][cx][sy], w0 = sm[1][cx][sy];
+    // warp w adds column w's strips, four a lane
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (w >= kSumCols) return;
+    float w1 = 0.f, w0 = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumStrips / 32; ++i) {
+        w1 += sm[0][lane + 32 * i][w];
+        w0 += sm[1][lane + 32 * i][w];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         w1 += __shfl_xor_sync(0xFFFFFFFFu, w1, o);
         w0 += __shfl_xor_sync(0xFFFFFFFFu, w0, o);
     }
-    const int col = blockIdx.x * 32 + sy;
-    if (cx == 0 && col < a.d) {
+    const int col = blockIdx.x * kSumCols + w;
+    if (lane == 0 && col < a.d) {
         const float gate = a.gate ? load_elem(a.gate, col, a.param_dt) : 1.f;
         if (a.dw) a.dw[col] = gate * w1;
         if (a.db) a.db[col] = gate * w0;
@@ -370,26 +517,88 @@ __global__ void __launch_bounds__(1024) norm_sum_kernel(const NormSumArgs a) {
     }
 }
 
-// Warps per row and groups of 8 per thread: as many warps as give each thread one
-// group, up to the block's 8.
-void shape_of(int d, int* wpr, int* nv) {
+// Warps per row, groups of 8 a thread, and the way in. Few rows (less than two warps for each of
+// the SMs' four schedulers): 8 warps a row, the shortest chain. Many: as few warps a row as hold it
+// with `most` groups a thread, so that a row's sums meet few warps; the copies ahead, not the warps,
+// keep HBM busy.
+struct Shape {
+    int w, nv, mode;
+};
+Shape shape_of(int T, int d, bool vec, int most) {
     const int v = (d + 7) / 8;
-    int w = 1;
-    while (w < kThreads / 32 && w * 32 < v) w *= 2;
-    *wpr = w;
-    int n = 1;
-    while (n * w * 32 < v) n *= 2;
-    *nv = n;
+    Shape s{1, 1, vec ? kStaged : kScalar};
+    while (s.w < 8 && s.w * 32 * most < v) s.w *= 2;
+    if (int64_t(T) * s.w < int64_t(num_sms()) * 8) {
+        s.w = 8;
+        if (vec) s.mode = kVec;
+    }
+    while (s.w * 32 * s.nv < v) s.nv *= 2;
+    if (s.mode == kStaged && s.w * 32 * s.nv * 8 == d) s.mode = kStagedFull;
+    return s;
 }
-static_assert(MOE_NORM_MAX_D <= 4 * 8 * kThreads, "a row fits four groups of 8 a thread");
+constexpr int kMostFwd = 4, kMostBwd = 2;  // the backward kernel also holds the sums over tokens
+static_assert(MOE_NORM_MAX_D <= 8 * 32 * 8 * 4, "a row fits a block");
 
-constexpr int kFwdBlocksPerSm = 8;
-// Backward blocks: the groups' partial sums are written and read once more, so few
-// enough that they stay small beside the rows.
-constexpr int kBwdBlocksPerSm = 4;
+// f with the shape as compile-time constants.
+template <int MOST, typename F>
+cudaError_t with_shape(const Shape& s, F f) {
+    using std::integral_constant;
+#define MOE_SHAPE(W_, NV_, M_)                    \
+    if (s.w == W_ && s.nv == NV_ && s.mode == M_) \
+        return f(integral_constant<int, W_>{}, integral_constant<int, NV_>{}, integral_constant<int, M_>{});
+#define MOE_SHAPES(W_, NV_) MOE_SHAPE(W_, NV_, kScalar) MOE_SHAPE(W_, NV_, kStaged) MOE_SHAPE(W_, NV_, kStagedFull)
+    MOE_SHAPE(8, 1, kVec) MOE_SHAPE(8, 2, kVec) MOE_SHAPE(8, 4, kVec)
+    MOE_SHAPE(8, 1, kScalar)
+    MOE_SHAPES(1, 1) MOE_SHAPES(1, 2) MOE_SHAPES(8, 4)
+    if constexpr (MOST == 4) {
+        MOE_SHAPES(1, 4) MOE_SHAPES(2, 4) MOE_SHAPES(4, 4)
+        MOE_SHAPE(8, 2, kScalar)
+    } else {
+        MOE_SHAPES(2, 2) MOE_SHAPES(4, 2) MOE_SHAPES(8, 2)
+    }
+#undef MOE_SHAPES
+#undef MOE_SHAPE
+    return cudaErrorInvalidValue;
+}
 
-int grid_of(int T, int wpr, int per_sm) {
-    const int rpb = kThreads / (32 * wpr);
+// Rows ahead: as many as a third of an SM's shared memory takes, two to four (three blocks an SM
+// where the registers allow).
+int depth_of(const Shape& s, size_t slot_bytes) {
+    return s.mode >= kStaged ? int(std::max<size_t>(2, std::min<size_t>(4, 72 * 1024 / slot_bytes))) : 0;
+}
+size_t pieces_bytes(int nv, int dt) { return size_t(nv) * (dt == MOE_DT_F32 ? 2 : 1) * 16 * kThreads; }
+
+constexpr int kMaxSmem = 200 * 1024;  // two rows of three fp32 tensors and the sums' place; a block may opt into 227 KB
+
+// The kernel may use more than 48 KB of shared memory (set once a device).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load() & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
+}
+
+// Blocks of a kernel that share an SM: a grid of just as many leaves no part of a second wave behind
+// (592 blocks where 444 fit took 34.7 us for 8192 rows of 4096 bf16, 444 blocks XX us).
+template <typename K>
+int blocks_per_sm(K kernel, size_t smem, std::atomic<uint64_t>& fit) {
+    const uint64_t known = fit.load();
+    if ((known >> 8) == smem + 1) return int(known & 255);
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, smem) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = 1;
+    }
+    fit.store((uint64_t(smem + 1) << 8) | uint64_t(n));
+    return n;
+}
+int grid_of(int T, int w, int per_sm) {
+    const int rpb = kThreads / (32 * w);
     const int64_t blocks = (int64_t(T) + rpb - 1) / rpb;
     return int(std::min<int64_t>(blocks, int64_t(num_sms()) * per_sm));
 }
@@ -398,9 +607,9 @@ size_t esize(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// 16-byte vectors on every row: the row's length and stride and the base.
+// Quads on every row: the row's length and stride and the base.
 bool rows_vec(const void* p, int d, int64_t ld, int dt) {
-    return !p || (d % 8 == 0 && (ld * int64_t(esize(dt))) % 16 == 0 && aligned(p, 16));
+    return !p || (d % 4 == 0 && ld % 4 == 0 && aligned(p, 4 * esize(dt)));
 }
 
 int check_params(const moe_norm_params* p) {
@@ -425,38 +634,48 @@ int64_t ld_of(int64_t ld, int d) { return ld ? ld : d; }
 
 bool elem_aligned(const void* p, int dt) { return aligned(p, esize(dt)); }
 
-template <bool POST, bool VEC>
-cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
-    int wpr, nv;
-    shape_of(a.d, &wpr, &nv);
-    const int grid = grid_of(a.T, wpr, kFwdBlocksPerSm);
+template <bool POST>
+cudaError_t launch_fwd(const NormArgs& a, bool vec, cudaStream_t s) {
+    const Shape sh = shape_of(a.T, a.d, vec, kMostFwd);
+    const size_t slot = POST ? pieces_bytes(sh.nv, a.block_dt) + pieces_bytes(sh.nv, a.stream_dt) : pieces_bytes(sh.nv, a.stream_dt);
+    const int depth = depth_of(sh, slot);
+    const size_t smem = depth * slot;
     ProfScope prof_(MOE_K_NORM, s);
-    const bool pdl = use_pdl(a.T);
-    switch (nv) {
-        case 1: return launch_pdl(pdl, norm_forward_kernel<1, VEC, POST>, dim3(grid), dim3(kThreads), 0, s, a, wpr);
-        case 2: return launch_pdl(pdl, norm_forward_kernel<2, VEC, POST>, dim3(grid), dim3(kThreads), 0, s, a, wpr);
-        default: return launch_pdl(pdl, norm_forward_kernel<4, VEC, POST>, dim3(grid), dim3(kThreads), 0, s, a, wpr);
-    }
+    return with_shape<kMostFwd>(sh, [&](auto W, auto NV, auto MODE) {
+        static std::atomic<uint64_t> done{0};
+        auto kernel = norm_forward_kernel<W(), NV(), MODE(), POST>;
+        const cudaError_t e = allow_smem(kernel, smem, done);
+        if (e != cudaSuccess) return e;
+        static std::atomic<uint64_t> fit{0};  // (shared memory, blocks an SM) of the last call
+        return launch_pdl(use_pdl(a.T), kernel, dim3(grid_of(a.T, sh.w, blocks_per_sm(kernel, smem, fit))), dim3(kThreads), smem, s,
+                          a, depth);
+    });
 }
 
-template <bool POST, bool VEC>
-cudaError_t launch_bwd(const NormBwdArgs& a, int grid, int wpr, int nv, cudaStream_t s) {
+template <bool POST, bool S0>
+cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& sh, int grid, cudaStream_t s) {
+    const size_t px = pieces_bytes(sh.nv, a.x_dt), slot = px + pieces_bytes(sh.nv, a.dy_dt) + (!POST && a.dres ? px : 0);
+    const int depth = depth_of(sh, slot);
+    const size_t sums = a.s1 && sh.w < kThreads / 32 ? size_t(a.d) * 4 * (S0 ? 2 : 1) : 0;
+    const size_t smem = std::max(depth * slot, sums);
     ProfScope prof_(MOE_K_NORM_BWD, s);
-    const bool pdl = use_pdl(a.T);
-    switch (nv) {
-        case 1: return launch_pdl(pdl, norm_backward_kernel<1, VEC, POST>, dim3(grid), dim3(kThreads), 0, s, a, wpr);
-        case 2: return launch_pdl(pdl, norm_backward_kernel<2, VEC, POST>, dim3(grid), dim3(kThreads), 0, s, a, wpr);
-        default: return launch_pdl(pdl, norm_backward_kernel<4, VEC, POST>, dim3(grid), dim3(kThreads), 0, s, a, wpr);
-    }
+    return with_shape<kMostBwd>(sh, [&](auto W, auto NV, auto MODE) {
+        static std::atomic<uint64_t> done{0};
+        auto kernel = norm_backward_kernel<W(), NV(), MODE(), POST, S0>;
+        const cudaError_t e = allow_smem(kernel, smem, done);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(use_pdl(a.T), kernel, dim3(grid), dim3(kThreads), smem, s, a, depth);
+    });
 }
 
-size_t norm_ws_bytes(const moe_norm_params* p) {
-    int wpr, nv;
-    shape_of(p->d, &wpr, &nv);
-    const int64_t groups = int64_t(grid_of(std::max(1, p->T), wpr, kBwdBlocksPerSm)) * (kThreads / (32 * wpr));
-    const size_t one = (size_t(groups) * p->d * 4 + 255) & ~size_t(255);
-    return 256 + 2 * one;
+// Room for the partial sums of either way in: the larger grid.
+size_t sums_bytes(const moe_norm_params* p) {
+    int grid = 0;
+    for (bool vec : {false, true})
+        grid = std::max(grid, grid_of(std::max(1, p->T), shape_of(std::max(1, p->T), p->d, vec, kMostBwd).w, kBwdBlocksMost));
+    return (size_t(grid) * p->d * 4 + 255) & ~size_t(255);
 }
+size_t norm_ws_bytes(const moe_norm_params* p) { return 256 + 2 * sums_bytes(p); }
 
 int check_f8_rows(const uint8_t* q8, const float* s8, int d, bool vec) {
     if (!q8 != !s8) return MOE_ERR_INVALID_ARG;
@@ -468,31 +687,29 @@ int check_f8_rows(const uint8_t* q8, const float* s8, int d, bool vec) {
 template <bool POST>
 int run_backward(const moe_norm_params* p, NormBwdArgs a, const moe_norm_grads& g, void* ws, size_t ws_bytes,
                  cudaStream_t stream, bool vec) {
-    int wpr, nv;
-    shape_of(p->d, &wpr, &nv);
-    const int grid = grid_of(p->T, wpr, kBwdBlocksPerSm);
-    const int groups = grid * (kThreads / (32 * wpr));
+    const Shape sh = shape_of(p->T, p->d, vec, kMostBwd);
     const bool gate_c = POST && p->gate_kind == MOE_GATE_CHANNEL;
     const bool need1 = g.dweight || (gate_c && g.dgate);
     const bool need0 = g.dbias || (gate_c && g.dgate && a.bias);
+    const int grid = grid_of(p->T, sh.w, bwd_blocks(sh.nv, need0));
     if (need1 || need0) {
         if (!ws) return MOE_ERR_INVALID_ARG;
         if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
         if (ws_bytes < norm_ws_bytes(p)) return MOE_ERR_WORKSPACE_TOO_SMALL;
-        const size_t one = (size_t(groups) * p->d * 4 + 255) & ~size_t(255);
         uint8_t* w = static_cast<uint8_t*>(ws) + 256;
-        if (need1) a.s1 = reinterpret_cast<float*>(w);
-        if (need0) a.s0 = reinterpret_cast<float*>(w + one);
+        a.s1 = reinterpret_cast<float*>(w);
+        if (need0) a.s0 = reinterpret_cast<float*>(w + sums_bytes(p));
     }
     a.dgate_tok = POST && p->gate_kind == MOE_GATE_TOKEN ? g.dgate : nullptr;
-    if ((vec ? launch_bwd<POST, true>(a, grid, wpr, nv, stream) : launch_bwd<POST, false>(a, grid, wpr, nv, stream)) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
+    const cudaError_t e = need0 ? launch_bwd<POST, true>(a, sh, grid, stream) : launch_bwd<POST, false>(a, sh, grid, stream);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (need1 || need0) {
         const NormSumArgs sa{a.s1, a.s0, a.weight, a.bias, gate_c ? a.gate : nullptr, g.dweight, g.dbias,
-                             gate_c ? g.dgate : nullptr, groups, p->d, p->param_dtype, p->weight_offset};
+                             gate_c ? g.dgate : nullptr, grid, p->d, p->param_dtype, p->weight_offset};
         ProfScope prof_(MOE_K_NORM_BWD, stream);
-        if (launch_pdl(use_pdl(p->T), norm_sum_kernel, dim3((p->d + 31) / 32), dim3(1024), 0, stream, sa) != cudaSuccess)
+        // its blocks may start as the rows' blocks end
+        if (launch_pdl(true, norm_sum_kernel, dim3((p->d + kSumCols - 1) / kSumCols), dim3(kSumCols * kSumStrips), 0,
+                       stream, sa) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -537,8 +754,7 @@ int moe_norm_forward(const moe_norm_params* p, const void* x, const void* weight
     a.ld_stream = lds; a.ld_block = ldb; a.T = p->T; a.d = p->d; a.kind = p->kind;
     a.stream_dt = p->stream_dtype; a.block_dt = p->block_dtype; a.param_dt = p->param_dtype;
     a.eps = p->eps; a.offset = p->weight_offset; a.alpha = 1.f; a.beta = 1.f;
-    return (vec ? launch_fwd<false, true>(a, stream) : launch_fwd<false, false>(a, stream)) == cudaSuccess ? MOE_OK
-                                                                                                           : MOE_ERR_CUDA;
+    return launch_fwd<false>(a, vec, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int moe_norm_backward(const moe_norm_params* p, const void* x, const void* weight, const void* dy, const void* dres,
@@ -604,8 +820,7 @@ int moe_norm_residual_forward(const moe_norm_params* p, const void* resid, const
     a.kind = p->kind; a.next_kind = p->next_kind; a.stream_dt = p->stream_dtype; a.block_dt = p->block_dtype;
     a.param_dt = p->param_dtype; a.gate_kind = p->gate_kind; a.eps = p->eps; a.offset = p->weight_offset;
     a.alpha = p->alpha; a.beta = p->beta;
-    return (vec ? launch_fwd<true, true>(a, stream) : launch_fwd<true, false>(a, stream)) == cudaSuccess ? MOE_OK
-                                                                                                         : MOE_ERR_CUDA;
+    return launch_fwd<true>(a, vec, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int moe_norm_residual_backward(const moe_norm_params* p, const void* y, const void* weight, const void* bias,

@@ -2,9 +2,9 @@
 // moe_quantize_f8 (rows, gathered by token for the experts' products) and
 // moe_quantize_f8_weights (once, at load time).
 //
-// Rows: a warp takes up to 1024 columns of a row, 8 to a lane and group of 256, with
-// all of its loads in flight first; 16 lanes find a block's largest magnitude by
-// shuffles and round it (rows.cuh). Bytes: 2 to 4 a value in, 1 out; a gathered
+// Rows: a warp takes up to 1024 columns of a row, a block of 128 at 4 columns a lane, with
+// all of its loads in flight first; one warp maximum finds a block's largest magnitude
+// (rows.cuh). Bytes: 2 to 4 a value in, 1 out; a gathered
 // row is read k times, from L2 for a prompt's x. Weights: a block of threads takes
 // one 128 x 128 block into registers; given [K, N] it turns it in shared memory.
 #include <algorithm>
@@ -58,17 +58,17 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int x
         const int dc = min(K - c0, 32 * 8 * kRowNV);
         const char* row = static_cast<const char*>(x) + (src * ld + c0) * (x_dt == MOE_DT_F32 ? 4 : 2);
         if (VEC) {
-            load_row<kRowNV, true>(v, row, dc, x_dt, 32, lane);
+            load_row<kRowNV, kVecRow>(v, row, dc, x_dt, 32, lane);
         } else {
 #pragma unroll
-            for (int i = 0; i < kRowNV; ++i) {
-                const int c = (i * 32 + lane) * 8;
+            for (int i = 0; i < kRowNV; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-                if (c < dc) load8<false>(v[i], row, c, x_dt);  // K is a multiple of 16
-            }
+                for (int j = 0; j < 8; ++j) {
+                    const int c = quad_at(i, j >> 2, 32, lane);
+                    v[i][j] = c < dc ? load_elem(row, c + (j & 3), x_dt) : 0.f;  // K is a multiple of 16
+                }
         }
-        store_row_e4m3<kRowNV>(v, q + r * K + c0, s + int64_t(c0 >> 7) * rows + r, rows, dc, 32, lane);
+        store_row_e4m3<kRowNV, kVecRow>(v, q + r * K + c0, s + int64_t(c0 >> 7) * rows + r, rows, dc, 32, lane);
     }
     if (bad) set_error(err, MOE_DEVERR_BOUNDS);
 }
@@ -109,10 +109,11 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, wmax[i]);
     const float sc = f8_scale(m);
+    const F8Div div(sc);
     if (threadIdx.x == 0) s[(int64_t(e) * gridDim.y + nb) * gridDim.x + kb] = sc;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint2 b = pack8_e4m3(v[i], sc);
+        const uint2 b = make_uint2(pack4_e4m3(v[i], div), pack4_e4m3(v[i] + 4, div));
         if (!TURN) {
             const int r = r0 + ry + 16 * i, c = c0 + cx;
             if (r < rows && c < cols) *reinterpret_cast<uint2*>(q + base + int64_t(r) * K + c) = b;
@@ -160,7 +161,7 @@ int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int
     const size_t es = x_dtype == MOE_DT_F32 ? 4 : 2;
     if (!aligned(q, 16) || !aligned(s, 4) || !aligned(x, es) || !aligned(row_index, 4) || !aligned(n_rows, 4))
         return MOE_ERR_MISALIGNED;
-    const bool vec = aligned(x, 16) && (ld * int64_t(es)) % 16 == 0;
+    const bool vec = aligned(x, 4 * es) && ld % 4 == 0;
     const int64_t chunks = (K + 32 * 8 * kRowNV - 1) / (32 * 8 * kRowNV);
     const int64_t blocks = std::min<int64_t>((rows * chunks + 7) / 8, int64_t(num_sms()) * 8);
     ProfScope prof_(MOE_K_QUANT_F8, stream);

@@ -3,6 +3,8 @@
 // 8-bit kernels (quantize_f8.cu, gated products).
 #pragma once
 
+#include <type_traits>
+
 #include "internal.h"
 
 namespace moe {
@@ -40,6 +42,16 @@ MOE_DEV void unpack8(const uint4& r, bool bf16, float (&v)[8]) {
         v[2 * i + 1] = bf16 ? bf16_hi(w[i]) : f16_hi(w[i]);
     }
 }
+MOE_DEV void unpack4(const uint2& r, bool bf16, float* v) {
+    v[0] = bf16 ? bf16_lo(r.x) : f16_lo(r.x);
+    v[1] = bf16 ? bf16_hi(r.x) : f16_hi(r.x);
+    v[2] = bf16 ? bf16_lo(r.y) : f16_lo(r.y);
+    v[3] = bf16 ? bf16_hi(r.y) : f16_hi(r.y);
+}
+MOE_DEV uint2 pack4(const float* v, bool bf16) {
+    return bf16 ? make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]))
+                : make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
+}
 MOE_DEV uint4 pack8(const float (&v)[8], bool bf16) {
     uint32_t w[4];
 #pragma unroll
@@ -48,108 +60,176 @@ MOE_DEV uint4 pack8(const float (&v)[8], bool bf16) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A row spread over `th` threads, NV groups of 8 elements each.
-//   VEC: group v of thread t holds the 8 consecutive elements at (v*th + t)*8
-//        (16-byte loads; the row's length is a multiple of 8 and every row
-//        starts on 16 bytes).
-//   else element j of group v sits at (v*8 + j)*th + t, so that any length,
-//        stride and alignment is read with neighbouring threads on
-//        neighbouring elements.
-// Elements past the row's end are zero and are not stored.
-template <int NV, bool VEC>
-MOE_DEV void load_row(float (&v)[NV][8], const void* row, int d, int dt, int th, int t) {
-    if (VEC) {
-        if (dt == MOE_DT_F32) {
-            float4 a[NV], b[NV];
+// A row spread over `th` threads, NV groups of 8 elements each: two quads of 4.
+//   kScalarRow: element j of group v sits at (v*8 + j)*th + t, so that any length, stride and
+//        alignment is read with neighbouring threads on neighbouring elements.
+//   kVecRow: quad q = 2v, 2v + 1 of thread t holds the 4 consecutive elements at (q*th + t)*4, so
+//        that a warp's access is 128 elements in a row whatever the dtype: 16 bytes a lane of fp32, 8
+//        of 16 bits (with 8 elements a lane, fp32 rows and weights took two accesses of every
+//        other 16 bytes each: half sectors). The row's length is a multiple of 4 and every row
+//        starts on 4 elements.
+//   kFullRow: the same for a row of exactly NV*th*8 elements: no quad needs its place checked.
+// Elements past the row's end are zero and are not stored. The dtype is looked at once a row, not
+// in the loops: with a branch a group these took more instructions than the arithmetic.
+enum RowLayout { kScalarRow = 0, kVecRow = 1, kFullRow = 2 };
+
+// The first column of quad h of group i, and whether it is inside the row.
+MOE_DEV int quad_at(int i, int h, int th, int t) { return ((2 * i + h) * th + t) * 4; }
+template <int L>
+MOE_DEV bool quad_in(int c, int d) {
+    return L == kFullRow || c < d;
+}
+template <int L, bool F32>
+MOE_DEV void load_group_as(float (&v)[8], const void* row, int i, int d, bool bf16, int th, int t) {
+    if (L != kScalarRow) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * th + t) * 8;
-                a[i] = b[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (c < d) {
-                    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
-                    a[i] = p[0];
-                    b[i] = p[1];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                v[i][0] = a[i].x; v[i][1] = a[i].y; v[i][2] = a[i].z; v[i][3] = a[i].w;
-                v[i][4] = b[i].x; v[i][5] = b[i].y; v[i][6] = b[i].z; v[i][7] = b[i].w;
-            }
-        } else {
-            uint4 r[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int c = (i * th + t) * 8;
-                r[i] = make_uint4(0, 0, 0, 0);
-                if (c < d) r[i] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(row) + c);
-            }
-            if (dt == MOE_DT_BF16) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) unpack8(r[i], true, v[i]);
+        for (int h = 0; h < 2; ++h) {
+            const int c = quad_at(i, h, th, t);
+            const bool in = quad_in<L>(c, d);
+            if (F32) {
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in) a = *reinterpret_cast<const float4*>(static_cast<const float*>(row) + c);
+                v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
             } else {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) unpack8(r[i], false, v[i]);
+                uint2 a = make_uint2(0, 0);
+                if (in) a = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(row) + c);
+                unpack4(a, bf16, v + 4 * h);
             }
         }
-    } else if (dt == MOE_DT_F32) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = (i * 8 + j) * th + t;
-                v[i][j] = c < d ? static_cast<const float*>(row)[c] : 0.f;
-            }
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = (i * 8 + j) * th + t;
+        for (int j = 0; j < 8; ++j) {
+            const int c = (i * 8 + j) * th + t;
+            if (F32) {
+                v[j] = c < d ? static_cast<const float*>(row)[c] : 0.f;
+            } else {
                 const uint16_t u = c < d ? static_cast<const uint16_t*>(row)[c] : uint16_t(0);
-                v[i][j] = dt == MOE_DT_BF16 ? bf16_to_f32(u) : f16_bits_to_f32(u);
+                v[j] = bf16 ? bf16_to_f32(u) : f16_bits_to_f32(u);
             }
+        }
     }
 }
 
-template <int NV, bool VEC>
-MOE_DEV void store_row(const float (&v)[NV][8], void* row, int d, int dt, int th, int t) {
-    if (VEC) {
+template <int NV, int L>
+MOE_DEV void load_row(float (&v)[NV][8], const void* row, int d, int dt, int th, int t) {
+    if (dt == MOE_DT_F32) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * th + t) * 8;
-            if (c >= d) continue;
-            if (dt == MOE_DT_F32) {
-                float4* p = reinterpret_cast<float4*>(static_cast<float*>(row) + c);
-                p[0] = make_float4(v[i][0], v[i][1], v[i][2], v[i][3]);
-                p[1] = make_float4(v[i][4], v[i][5], v[i][6], v[i][7]);
-            } else {
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c) = pack8(v[i], dt == MOE_DT_BF16);
-            }
-        }
-    } else if (dt == MOE_DT_F32) {
+        for (int i = 0; i < NV; ++i) load_group_as<L, true>(v[i], row, i, d, false, th, t);
+    } else if (dt == MOE_DT_BF16) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int c = (i * 8 + j) * th + t;
-                if (c < d) static_cast<float*>(row)[c] = v[i][j];
-            }
+        for (int i = 0; i < NV; ++i) load_group_as<L, false>(v[i], row, i, d, true, th, t);
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i) load_group_as<L, false>(v[i], row, i, d, false, th, t);
+    }
+}
+
+template <int NV, int L, bool F32>
+MOE_DEV void store_row_as(const float (&v)[NV][8], void* row, int d, bool bf16, int th, int t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (L != kScalarRow) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = quad_at(i, h, th, t);
+                if (!quad_in<L>(c, d)) continue;
+                if (F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(row) + c) =
+                        make_float4(v[i][4 * h], v[i][4 * h + 1], v[i][4 * h + 2], v[i][4 * h + 3]);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(row) + c) = pack4(v[i] + 4 * h, bf16);
+            }
+        } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int c = (i * 8 + j) * th + t;
-                if (c < d) store_elem(row, c, v[i][j], dt);
+                if (c < d) {
+                    if (F32) static_cast<float*>(row)[c] = v[i][j];
+                    else store_elem(row, c, v[i][j], bf16 ? MOE_DT_BF16 : MOE_DT_F16);
+                }
             }
+        }
     }
+}
+template <int NV, int L>
+MOE_DEV void store_row(const float (&v)[NV][8], void* row, int d, int dt, int th, int t) {
+    if (dt == MOE_DT_F32) store_row_as<NV, L, true>(v, row, d, false, th, t);
+    else if (dt == MOE_DT_BF16) store_row_as<NV, L, false>(v, row, d, true, th, t);
+    else store_row_as<NV, L, false>(v, row, d, false, th, t);
+}
+
+// f with the dtype as a compile-time constant (0 fp32, 1 bf16, 2 fp16): one branch around a loop.
+template <typename F>
+MOE_DEV void by_dtype(int dt, F f) {
+    if (dt == MOE_DT_F32) f(std::integral_constant<int, 0>{});
+    else if (dt == MOE_DT_BF16) f(std::integral_constant<int, 1>{});
+    else f(std::integral_constant<int, 2>{});
+}
+template <int L, int DT>
+MOE_DEV void load_group(float (&v)[8], const void* row, int i, int d, int th, int t) {
+    load_group_as<L, DT == MOE_DT_F32>(v, row, i, d, DT == MOE_DT_BF16, th, t);
 }
 
 // Whether element (group i, place j) of thread t lies inside a row of d elements.
-template <bool VEC>
+template <int L>
 MOE_DEV bool in_row(int i, int j, int d, int th, int t) {
-    return (VEC ? (i * th + t) * 8 + j : (i * 8 + j) * th + t) < d;
+    if (L == kScalarRow) return (i * 8 + j) * th + t < d;
+    return quad_in<L>(quad_at(i, j >> 2, th, t), d);
+}
+
+// ---- rows on their way through shared memory (vector layouts). Each thread copies the quads that
+// it will read itself, so nothing but its own wait for them is needed; quad q of the block's thread t
+// sits at q * threads + t. Room for a row of a tensor: stage_pieces() * 16 bytes a thread.
+__host__ __device__ inline int stage_pieces(int nv, int dt) { return nv * (dt == MOE_DT_F32 ? 2 : 1); }
+
+MOE_DEV void cp_async_8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+// base: the tensor's place in the stage (thread 0's).
+template <int NV, int L, int THREADS>
+MOE_DEV void copy_row(uint32_t base, const char* row, int d, int dt, int th, int t) {
+    if (dt == MOE_DT_F32) {
+#pragma unroll
+        for (int q = 0; q < 2 * NV; ++q) {
+            const int c = (q * th + t) * 4;
+            if (quad_in<L>(c, d)) cp_async_16(base + (q * THREADS + threadIdx.x) * 16, row + c * 4, 16);
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2 * NV; ++q) {
+            const int c = (q * th + t) * 4;
+            if (quad_in<L>(c, d)) cp_async_8(base + (q * THREADS + threadIdx.x) * 8, row + c * 2);
+        }
+    }
+}
+template <int NV, int L, int THREADS>
+MOE_DEV void read_row(float (&v)[NV][8], const uint4* base, int d, int dt, int th, int t) {
+    by_dtype(dt, [&](auto DT) {
+#pragma unroll
+        for (int q = 0; q < 2 * NV; ++q) {
+            const bool in = quad_in<L>((q * th + t) * 4, d);
+            float* w = v[q >> 1] + 4 * (q & 1);
+            if (decltype(DT)::value == MOE_DT_F32) {
+                uint4 a = make_uint4(0, 0, 0, 0);
+                if (in) a = base[q * THREADS + threadIdx.x];
+                w[0] = __uint_as_float(a.x); w[1] = __uint_as_float(a.y);
+                w[2] = __uint_as_float(a.z); w[3] = __uint_as_float(a.w);
+            } else {
+                uint2 a = make_uint2(0, 0);
+                if (in) a = reinterpret_cast<const uint2*>(base)[q * THREADS + threadIdx.x];
+                unpack4(a, decltype(DT)::value == MOE_DT_BF16, w);
+            }
+        }
+    });
+}
+// At most n of this thread's committed groups of copies still on their way (n < 4).
+MOE_DEV void cp_async_wait_most(int n) {
+    switch (n) {
+        case 0: cp_async_wait<0>(); break;
+        case 1: cp_async_wait<1>(); break;
+        case 2: cp_async_wait<2>(); break;
+        default: cp_async_wait<3>(); break;
+    }
 }
 
 // ------------------------------------------------------------------ e4m3 with a scale
@@ -191,39 +271,30 @@ struct F8Div {
         return fmaf(-fmaf(q, s, -x), rs, q);  // the remainder with this sign keeps -0
     }
 };
-// Eight values of a group whose scale is s.
-MOE_DEV uint2 pack8_e4m3(const float (&v)[8], float s) {
-    const F8Div div(s);
-    uint32_t h[4];
-    if (div.fast) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = pack_e4m3x2(div(v[2 * i]), div(v[2 * i + 1]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = pack_e4m3x2(__fdiv_rn(v[2 * i], s), __fdiv_rn(v[2 * i + 1], s));
-    }
-    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+// Four values of a group whose scale is s.
+MOE_DEV uint32_t pack4_e4m3(const float* v, const F8Div& div) {
+    return div.fast ? pack_e4m3x2(div(v[0]), div(v[1])) | pack_e4m3x2(div(v[2]), div(v[3])) << 16
+                    : pack_e4m3x2(__fdiv_rn(v[0], div.s), __fdiv_rn(v[1], div.s)) |
+                          pack_e4m3x2(__fdiv_rn(v[2], div.s), __fdiv_rn(v[3], div.s)) << 16;
 }
 
-// A row in the VEC layout to e4m3: 16 neighbouring threads hold a group of 128
-// columns. q: the row's bytes; s: scale of column group 0, the next ones `lds` on.
-// Every thread of the warp takes part.
-template <int NV>
+// A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes;
+// s: scale of column group 0, the next ones `lds` on. Every thread of the warp takes part.
+template <int NV, int L>
 MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64_t lds, int d, int th, int t) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * th + t) * 8;
-        uint32_t m = 0;
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float sc = f8_scale(m);
-        if (c < d) {
-            *reinterpret_cast<uint2*>(q + c) = pack8_e4m3(v[i], sc);
-            if ((t & 15) == 0) s[int64_t(c >> 7) * lds] = sc;
+        for (int h = 0; h < 2; ++h) {
+            const float* x = v[i] + 4 * h;
+            const uint32_t m = max(max(abs_bits(x[0]), abs_bits(x[1])), max(abs_bits(x[2]), abs_bits(x[3])));
+            const F8Div div(f8_scale(__reduce_max_sync(0xFFFFFFFFu, m)));
+            const int c = quad_at(i, h, th, t);
+            if (quad_in<L>(c, d)) {
+                *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(x, div);
+                if ((t & 31) == 0) s[int64_t(c >> 7) * lds] = div.s;
+            }
         }
-    }
 }
 
 }  // namespace moe

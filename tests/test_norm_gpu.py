@@ -57,7 +57,10 @@ def rows_of(t, ld, shift=0):
 SIZES = [(1, 1, 0, 0, 0.0, 0.0), (1, 8, 0, 0, 0.0, 1.0), (3, 7, 0, 0, 0.0, 0.0), (5, 128, 0, 0, 4.0, 0.0),
          (37, 129, 0, 0, 0.0, 0.0), (9, 255, 300, 0, 0.0, 1.0), (33, 256, 264, 8, 0.0, 0.0), (17, 1000, 0, 1, 0.0, 0.0),
          (300, 1024, 0, 0, 30.0, 0.0), (64, 2048, 0, 0, 0.0, 0.0), (2, 4096, 0, 0, 0.0, 1.0), (3, 4100, 0, 0, 0.0, 0.0),
-         (2, 8192, 0, 0, 0.0, 0.0), (2, 8191, 0, 0, 1.0, 0.0), (1700, 320, 0, 0, 0.0, 0.0)]
+         (2, 8192, 0, 0, 0.0, 0.0), (2, 8191, 0, 0, 1.0, 0.0), (1700, 320, 0, 0, 0.0, 0.0),
+         # many rows: the rows ahead pass through shared memory, with 1, 2, 4 and 8 warps a row
+         (1201, 248, 0, 0, 0.0, 0.0), (1251, 1024, 1032, 8, 0.0, 0.0), (613, 2048, 0, 0, 2.0, 0.0), (301, 4096, 0, 0, 0.0, 1.0),
+         (151, 8192, 0, 0, 0.0, 0.0), (601, 2040, 0, 0, 0.0, 0.0), (1300, 1023, 0, 0, 0.0, 0.0), (160, 8185, 0, 0, 0.0, 0.0)]
 
 
 def tol_norm(x, kind, w, bias, offset):
@@ -112,7 +115,8 @@ def test_before(size, stream, block, par, kind):
 @pytest.mark.parametrize("gate", ["none", "channel", "token"])
 @pytest.mark.parametrize("stream,block", [("f32", "bf16"), ("bf16", "f16")])
 @pytest.mark.parametrize("size", [(1, 3, 0, 0), (5, 64, 0, 0), (37, 129, 0, 0), (9, 1000, 1008, 8), (130, 1024, 0, 0),
-                                  (3, 4096, 0, 0), (21, 2047, 2100, 3), (2, 8192, 0, 0), (2, 6001, 0, 0)])
+                                  (3, 4096, 0, 0), (21, 2047, 2100, 3), (2, 8192, 0, 0), (2, 6001, 0, 0),
+                                  (1251, 512, 0, 0), (620, 2048, 2056, 0), (303, 4096, 0, 0), (152, 8192, 0, 0), (640, 1999, 0, 0)])
 def test_after(size, stream, block, gate, kind):
     T, d, ld, shift = size
     rng = np.random.default_rng([T, d, 1])
