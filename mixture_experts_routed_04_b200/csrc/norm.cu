@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_forward_kernel(const NormArg
         float res[POST ? NV : 1][8];
         if constexpr (STAGED) {
             cp_async_wait_most(depth - 1);
+            __syncwarp();  // a lane's quads may be another lane's copies
             const uint4* src = stage + slot * pieces * kThreads;
             read_row<NV, L, kThreads>(v, src, dl, x_dt, th, t);
             if constexpr (POST) read_row<NV, L, kThreads>(res, src + px * kThreads, dl, a.stream_dt, th, t);
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_forward_kernel(const NormArg
             if (a.q8) store_row_e4m3<NV, L == kScalarRow ? kVecRow : L>(v, a.q8 + (live ? r : 0) * d, a.s8 + (live ? r : 0), a.T, dl, th, t);
         }
         if constexpr (STAGED) {  // the row is in registers: its place takes the row `depth` on
+            __syncwarp();
             fetch(slot, r + depth * step);
             slot = slot + 1 == depth ? 0 : slot + 1;
         }
@@ -271,13 +273,15 @@ struct NormBwdArgs {
 };
 
 // Backward blocks an SM (their registers): also the grid, whose partial sums are written and read once
-// more, so few enough that they stay small beside the rows.
-__host__ __device__ constexpr int bwd_blocks(int nv, bool s0) { return nv <= 2 && !s0 ? 3 : 2; }
-constexpr int kBwdBlocksMost = 3;
+// more, so few enough that they stay small beside the rows. In vectors the copies ahead keep HBM busy
+// (4096 rows of 2048 bf16: 18.2 us with 2 blocks and 96 registers, 21.2 with 3, 27.5 with 4, whose
+// registers do not hold a row); element by element the warps do (rows of 2047: 67.8, 56.0, 47.9 us).
+__host__ __device__ constexpr int bwd_blocks(int nv, int mode) { return mode == kScalar && nv <= 2 ? 4 : 2; }
+constexpr int kBwdBlocksMost = 4;
 
 // S0: whether sums without xhat are wanted (a bias).
 template <int W, int NV, int MODE, bool POST, bool S0>
-__global__ void __launch_bounds__(kThreads, bwd_blocks(NV, S0)) norm_backward_kernel(const NormBwdArgs a, const int depth) {
+__global__ void __launch_bounds__(kThreads, bwd_blocks(NV, MODE)) norm_backward_kernel(const NormBwdArgs a, const int depth) {
     constexpr int L = layout_of(MODE);
     constexpr bool STAGED = MODE >= kStaged;
     constexpr int th = 32 * W, rpb = kThreads / th;
@@ -320,6 +324,7 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(NV, S0)) norm_backward_ke
         const uint4* src = stage + slot * pieces * kThreads;
         if constexpr (STAGED) {
             cp_async_wait_most(depth - 1);
+            __syncwarp();  // a lane's quads may be another lane's copies
             read_row<NV, L, kThreads>(x, src, dl, a.x_dt, th, t);
             read_row<NV, L, kThreads>(g, src + px * kThreads, dl, a.dy_dt, th, t);
             if (L == kFullRow && !live) {  // nothing was copied for a row past T
@@ -414,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, bwd_blocks(NV, S0)) norm_backward_ke
         }
         if (live) store_row<NV, L>(g, at_row(a.dx, r, a.ld_x, a.x_dt), d, a.x_dt, th, t);
         if constexpr (STAGED) {
+            __syncwarp();
             fetch(slot, r + depth * step);
             slot = slot + 1 == depth ? 0 : slot + 1;
         }
@@ -524,11 +530,11 @@ __global__ void __launch_bounds__(kSumCols* kSumStrips) norm_sum_kernel(const No
 struct Shape {
     int w, nv, mode;
 };
-Shape shape_of(int T, int d, bool vec, int most) {
+Shape shape_of(int T, int d, int vec, int most) {  // vec: rows_vec of every tensor
     const int v = (d + 7) / 8;
-    Shape s{1, 1, vec ? kStaged : kScalar};
+    Shape s{1, 1, vec == 2 ? kStaged : kScalar};
     while (s.w < 8 && s.w * 32 * most < v) s.w *= 2;
-    if (int64_t(T) * s.w < int64_t(num_sms()) * 8) {
+    if (vec == 1 || int64_t(T) * s.w < int64_t(num_sms()) * 8) {
         s.w = 8;
         if (vec) s.mode = kVec;
     }
@@ -607,9 +613,12 @@ size_t esize(int dt) { return dt == MOE_DT_F32 ? 4 : 2; }
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Quads on every row: the row's length and stride and the base.
-bool rows_vec(const void* p, int d, int64_t ld, int dt) {
-    return !p || (d % 4 == 0 && ld % 4 == 0 && aligned(p, 4 * esize(dt)));
+// How far rows can be read in vectors: 1 quads on every row (its length and stride and the base), 2
+// also every row on 16 bytes, 0 neither.
+int rows_vec(const void* p, int d, int64_t ld, int dt) {
+    if (!p) return 2;
+    if (d % 4 || ld % 4 || !aligned(p, 4 * esize(dt))) return 0;
+    return (ld * int64_t(esize(dt))) % 16 == 0 && aligned(p, 16) ? 2 : 1;
 }
 
 int check_params(const moe_norm_params* p) {
@@ -635,7 +644,7 @@ int64_t ld_of(int64_t ld, int d) { return ld ? ld : d; }
 bool elem_aligned(const void* p, int dt) { return aligned(p, esize(dt)); }
 
 template <bool POST>
-cudaError_t launch_fwd(const NormArgs& a, bool vec, cudaStream_t s) {
+cudaError_t launch_fwd(const NormArgs& a, int vec, cudaStream_t s) {
     const Shape sh = shape_of(a.T, a.d, vec, kMostFwd);
     const size_t slot = POST ? pieces_bytes(sh.nv, a.block_dt) + pieces_bytes(sh.nv, a.stream_dt) : pieces_bytes(sh.nv, a.stream_dt);
     const int depth = depth_of(sh, slot);
@@ -671,13 +680,13 @@ cudaError_t launch_bwd(const NormBwdArgs& a, const Shape& sh, int grid, cudaStre
 // Room for the partial sums of either way in: the larger grid.
 size_t sums_bytes(const moe_norm_params* p) {
     int grid = 0;
-    for (bool vec : {false, true})
+    for (int vec : {0, 1, 2})
         grid = std::max(grid, grid_of(std::max(1, p->T), shape_of(std::max(1, p->T), p->d, vec, kMostBwd).w, kBwdBlocksMost));
     return (size_t(grid) * p->d * 4 + 255) & ~size_t(255);
 }
 size_t norm_ws_bytes(const moe_norm_params* p) { return 256 + 2 * sums_bytes(p); }
 
-int check_f8_rows(const uint8_t* q8, const float* s8, int d, bool vec) {
+int check_f8_rows(const uint8_t* q8, const float* s8, int d, int vec) {
     if (!q8 != !s8) return MOE_ERR_INVALID_ARG;
     if (!q8) return MOE_OK;
     if (d % 16) return MOE_ERR_INVALID_ARG;
@@ -686,12 +695,12 @@ int check_f8_rows(const uint8_t* q8, const float* s8, int d, bool vec) {
 
 template <bool POST>
 int run_backward(const moe_norm_params* p, NormBwdArgs a, const moe_norm_grads& g, void* ws, size_t ws_bytes,
-                 cudaStream_t stream, bool vec) {
+                 cudaStream_t stream, int vec) {
     const Shape sh = shape_of(p->T, p->d, vec, kMostBwd);
     const bool gate_c = POST && p->gate_kind == MOE_GATE_CHANNEL;
     const bool need1 = g.dweight || (gate_c && g.dgate);
     const bool need0 = g.dbias || (gate_c && g.dgate && a.bias);
-    const int grid = grid_of(p->T, sh.w, bwd_blocks(sh.nv, need0));
+    const int grid = grid_of(p->T, sh.w, bwd_blocks(sh.nv, sh.mode));
     if (need1 || need0) {
         if (!ws) return MOE_ERR_INVALID_ARG;
         if (!aligned(ws, 256)) return MOE_ERR_MISALIGNED;
@@ -746,8 +755,9 @@ int moe_norm_forward(const moe_norm_params* p, const void* x, const void* weight
     if (!elem_aligned(x, p->stream_dtype) || !elem_aligned(y, p->block_dtype) || !elem_aligned(weight, p->param_dtype) ||
         !elem_aligned(bias, p->param_dtype) || !aligned(mean, 4) || !aligned(rstd, 4))
         return MOE_ERR_MISALIGNED;
-    const bool vec = rows_vec(x, p->d, lds, p->stream_dtype) && rows_vec(y, p->d, ldb, p->block_dtype) &&
-                     rows_vec(weight, p->d, p->d, p->param_dtype) && rows_vec(bias, p->d, p->d, p->param_dtype);
+    int vec = std::min(rows_vec(x, p->d, lds, p->stream_dtype), rows_vec(y, p->d, ldb, p->block_dtype));
+    for (const void* v : {weight, bias})
+        if (!rows_vec(v, p->d, p->d, p->param_dtype)) vec = 0;
     if ((st = check_f8_rows(q8, s8, p->d, vec)) != MOE_OK) return st;
     NormArgs a{};
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.q8 = q8; a.s8 = s8; a.mean = mean; a.rstd = rstd;
@@ -776,9 +786,9 @@ int moe_norm_backward(const moe_norm_params* p, const void* x, const void* weigh
         !elem_aligned(weight, p->param_dtype) || !elem_aligned(dres, p->stream_dtype) ||
         !elem_aligned(dx, p->stream_dtype) || !aligned(mean, 4) || !aligned(rstd, 4))
         return MOE_ERR_MISALIGNED;
-    const bool vec = rows_vec(x, p->d, lds, p->stream_dtype) && rows_vec(dy, p->d, ldb, p->block_dtype) &&
-                     rows_vec(weight, p->d, p->d, p->param_dtype) && rows_vec(dres, p->d, lds, p->stream_dtype) &&
-                     rows_vec(dx, p->d, lds, p->stream_dtype);
+    int vec = rows_vec(dy, p->d, ldb, p->block_dtype);
+    for (const void* v : {x, dres, static_cast<const void*>(dx)}) vec = std::min(vec, rows_vec(v, p->d, lds, p->stream_dtype));
+    if (!rows_vec(weight, p->d, p->d, p->param_dtype)) vec = 0;
     NormBwdArgs a{};
     a.x = x; a.dy = dy; a.dres = dres; a.weight = weight; a.mean = mean; a.rstd = rstd; a.dx = dx;
     a.ld_x = lds; a.ld_dy = ldb; a.T = p->T; a.d = p->d; a.kind = p->kind;
@@ -808,10 +818,10 @@ int moe_norm_residual_forward(const moe_norm_params* p, const void* resid, const
         if (!elem_aligned(v, p->param_dtype)) return MOE_ERR_MISALIGNED;
     for (const float* v : {mean, rstd, next_mean, next_rstd})
         if (!aligned(v, 4)) return MOE_ERR_MISALIGNED;
-    bool vec = rows_vec(resid, p->d, lds, p->stream_dtype) && rows_vec(out, p->d, lds, p->stream_dtype) &&
-               rows_vec(y, p->d, ldb, p->block_dtype) && rows_vec(x_next, p->d, ldb, p->block_dtype);
+    int vec = std::min({rows_vec(resid, p->d, lds, p->stream_dtype), rows_vec(out, p->d, lds, p->stream_dtype),
+                        rows_vec(y, p->d, ldb, p->block_dtype), rows_vec(x_next, p->d, ldb, p->block_dtype)});
     for (const void* v : {weight, bias, p->gate_kind == MOE_GATE_CHANNEL ? gate : nullptr, next_weight, next_bias})
-        vec = vec && rows_vec(v, p->d, p->d, p->param_dtype);
+        if (!rows_vec(v, p->d, p->d, p->param_dtype)) vec = 0;
     if ((st = check_f8_rows(q8, s8, p->d, vec)) != MOE_OK) return st;
     NormArgs a{};
     a.x = y; a.resid = resid; a.weight = weight; a.bias = bias; a.gate = gate; a.next_weight = next_weight;
@@ -846,10 +856,10 @@ int moe_norm_residual_backward(const moe_norm_params* p, const void* y, const vo
     for (const void* v : {weight, bias, gate})
         if (!elem_aligned(v, p->param_dtype)) return MOE_ERR_MISALIGNED;
     if (!aligned(mean, 4) || !aligned(rstd, 4)) return MOE_ERR_MISALIGNED;
-    bool vec = rows_vec(y, p->d, ldb, p->block_dtype) && rows_vec(dy, p->d, ldb, p->block_dtype) &&
-               rows_vec(dout, p->d, lds, p->stream_dtype) && rows_vec(dresid, p->d, lds, p->stream_dtype);
+    int vec = std::min({rows_vec(y, p->d, ldb, p->block_dtype), rows_vec(dy, p->d, ldb, p->block_dtype),
+                        rows_vec(dout, p->d, lds, p->stream_dtype), rows_vec(dresid, p->d, lds, p->stream_dtype)});
     for (const void* v : {weight, bias, p->gate_kind == MOE_GATE_CHANNEL ? gate : nullptr})
-        vec = vec && rows_vec(v, p->d, p->d, p->param_dtype);
+        if (!rows_vec(v, p->d, p->d, p->param_dtype)) vec = 0;
     NormBwdArgs a{};
     a.x = y; a.dy = dout; a.weight = weight; a.bias = bias; a.gate = gate; a.mean = mean; a.rstd = rstd; a.dx = dy;
     a.dresid = dresid; a.ld_x = ldb; a.ld_dy = lds; a.T = p->T; a.d = p->d; a.kind = p->kind;

@@ -32,69 +32,115 @@ MOE_DEV void load8(float (&v)[8], const void* p, int64_t i, int dt) {
     }
 }
 
-template <bool VEC>
+// RPW: rows a warp. 8 (many rows): their scales of a block of columns lie next to each other and
+// leave as whole sectors, where one row a warp writes 4 bytes of a sector at a time, as many of those
+// as there are 128-byte pieces of q. 1 (few rows): a warp takes 1024 columns of a row.
+constexpr int kChunk = 32 * 8 * kRowNV;  // columns a warp holds at once
+constexpr int kSpan = 32 * 128;          // columns whose scales a warp holds, one a lane
+
+template <bool VEC, int RPW>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int x_dt, int64_t ld, int64_t src_rows,
-                                                            const int32_t* row_index, const int32_t* n_rows,
-                                                            int64_t rows, int K, uint8_t* q, float* s, uint32_t* err) {
+                                                            const int32_t* row_index, const int32_t* n_rows, int rows,
+                                                            int K, uint8_t* q, float* s, uint32_t* err) {
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31;
-    const int chunks = (K + 32 * 8 * kRowNV - 1) / (32 * 8 * kRowNV);
-    const int64_t n = n_rows ? min(rows, int64_t(max(0, *n_rows))) : rows;
-    const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
+    const int n = n_rows ? min(rows, max(0, *n_rows)) : rows;
+    const bool wide = (reinterpret_cast<uintptr_t>(s) & 15) == 0;
+    const int units = RPW > 1 ? (n + RPW - 1) / RPW : n;
+    const int warps = gridDim.x * (blockDim.x >> 5);
     bool bad = false;
-    for (int64_t u = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < n * chunks; u += warps) {
-        const int64_t r = u / chunks;
-        const int c0 = int(u - r * chunks) * (32 * 8 * kRowNV);
-        int64_t src = r;
-        if (row_index) {
-            src = row_index[r];
-            if (src < 0 || src >= src_rows) {
-                bad = true;
-                continue;
+    // RPW 1: the grid's second dimension is the chunk of columns
+    for (int64_t u = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < units; u += warps) {
+        const int r0 = int(u) * RPW, nr = min(RPW, n - r0);
+        int src = -1;
+        if (lane < nr) {
+            src = r0 + lane;
+            if (row_index) {
+                src = row_index[r0 + lane];
+                if (src < 0 || src >= src_rows) {
+                    bad = true;
+                    src = -1;
+                }
             }
         }
-        float v[kRowNV][8];
-        const int dc = min(K - c0, 32 * 8 * kRowNV);
-        const char* row = static_cast<const char*>(x) + (src * ld + c0) * (x_dt == MOE_DT_F32 ? 4 : 2);
-        if (VEC) {
-            load_row<kRowNV, kVecRow>(v, row, dc, x_dt, 32, lane);
-        } else {
+        const uint32_t ok = __ballot_sync(0xFFFFFFFFu, src >= 0);  // rows to write
+        for (int c0 = RPW > 1 ? 0 : int(blockIdx.y) * kChunk; c0 < (RPW > 1 ? K : min(K, int(blockIdx.y + 1) * kChunk));
+             c0 += kSpan) {
+            float sc[RPW];  // lane: group of columns c0 / 128 + lane
 #pragma unroll
-            for (int i = 0; i < kRowNV; ++i)
+            for (int i = 0; i < RPW; ++i) {
+                sc[i] = 0.f;
+                const int row = __shfl_sync(0xFFFFFFFFu, src, i);
+                if (row < 0) continue;
+                const int end = RPW > 1 ? min(K, c0 + kSpan) : min(K, c0 + kChunk);
+                for (int c = c0; c < end; c += kChunk) {
+                    float v[kRowNV][8];
+                    const int dc = min(end - c, kChunk);
+                    const char* p = static_cast<const char*>(x) + (row * ld + c) * (x_dt == MOE_DT_F32 ? 4 : 2);
+                    if (VEC) {
+                        if (dc == kChunk) load_row<kRowNV, kFullRow>(v, p, dc, x_dt, 32, lane);
+                        else load_row<kRowNV, kVecRow>(v, p, dc, x_dt, 32, lane);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int c = quad_at(i, j >> 2, 32, lane);
-                    v[i][j] = c < dc ? load_elem(row, c + (j & 3), x_dt) : 0.f;  // K is a multiple of 16
+                        for (int k = 0; k < kRowNV; ++k)
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const int cc = quad_at(k, j >> 2, 32, lane);
+                                v[k][j] = cc < dc ? load_elem(p, cc + (j & 3), x_dt) : 0.f;  // K is a multiple of 16
+                            }
+                    }
+                    uint8_t* qr = q + int64_t(r0 + i) * K + c;
+#pragma unroll
+                    for (int k = 0; k < 2 * kRowNV; ++k) {
+                        const float* w = v[k >> 1] + 4 * (k & 1);
+                        const uint32_t m = max(max(abs_bits(w[0]), abs_bits(w[1])), max(abs_bits(w[2]), abs_bits(w[3])));
+                        const F8Div div(f8_scale(__reduce_max_sync(0xFFFFFFFFu, m)));
+                        const int cc = (k * 32 + lane) * 4;
+                        if (cc < dc) *reinterpret_cast<uint32_t*>(qr + cc) = pack4_e4m3(w, div);
+                        if (lane == ((c - c0) >> 7) + k) sc[i] = div.s;
+                    }
                 }
+            }
+            const int g = c0 / 128 + lane;
+            if (g * 128 < K && (RPW > 1 || lane < kChunk / 128)) {
+                float* sp = s + int64_t(g) * rows + r0;
+                if (RPW == 8 && ok == 0xFFu && rows % 4 == 0 && wide) {
+                    reinterpret_cast<float4*>(sp)[0] = make_float4(sc[0], sc[1 % RPW], sc[2 % RPW], sc[3 % RPW]);
+                    reinterpret_cast<float4*>(sp)[1] = make_float4(sc[4 % RPW], sc[5 % RPW], sc[6 % RPW], sc[7 % RPW]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < RPW; ++i)
+                        if (ok >> i & 1u) sp[i] = sc[i];
+                }
+            }
         }
-        store_row_e4m3<kRowNV, kVecRow>(v, q + r * K + c0, s + int64_t(c0 >> 7) * rows + r, rows, dc, 32, lane);
     }
     if (bad) set_error(err, MOE_DEVERR_BOUNDS);
 }
 
-constexpr int kTurnPitch = 132;  // bytes of a turned row in shared memory: neighbouring rows 33 banks apart
-
-// One 128 x 128 block of a matrix of `rows` x `cols` (row-major): thread t holds
-// the 8 columns (t & 15) * 8 of rows (t >> 4) + 16 i. TURN: the matrix is [K, N]
-// and the result its transpose.
+// One 128 x 128 block of a matrix of `rows` x `cols` (row-major): thread t holds the 8 columns
+// (t & 15) * 8 of the 8 rows (t >> 4) * 8 on. TURN: the matrix is [K, N] and the result its transpose;
+// a thread's 8 values along K of a column are 8 neighbouring bytes of it, rounded two at a time along
+// K, and pass through shared memory: chunk c of column n's 128 bytes at n*128 + 8 (c ^ n/8 % 16), so
+// that a half warp's writes, eight columns apart, fall in all the banks.
 template <bool VEC, bool TURN>
 __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, int w_dt, int N, int K, uint8_t* q,
                                                                float* s) {
     __shared__ uint32_t wmax[8];
-    __shared__ __align__(16) uint8_t turn[TURN ? 128 * kTurnPitch : 16];
+    __shared__ __align__(16) uint8_t turn[TURN ? 128 * 128 : 16];
     griddep_wait();
     griddep_launch();
     const int e = blockIdx.z, nb = blockIdx.y, kb = blockIdx.x;
     const int rows = TURN ? K : N, cols = TURN ? N : K;
     const int r0 = (TURN ? kb : nb) * 128, c0 = (TURN ? nb : kb) * 128;
-    const int cx = (threadIdx.x & 15) * 8, ry = threadIdx.x >> 4;
+    const int cx = (threadIdx.x & 15) * 8, ry = (threadIdx.x >> 4) * 8;
     const int64_t base = int64_t(e) * N * K;
     float v[8][8];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int r = r0 + ry + 16 * i, c = c0 + cx;
+        const int r = r0 + ry + i, c = c0 + cx;
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
         if (r < rows && c < cols) load8<VEC>(v[i], w, base + int64_t(r) * cols + c, w_dt);  // cols: a multiple of 8
@@ -111,26 +157,30 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, in
     const float sc = f8_scale(m);
     const F8Div div(sc);
     if (threadIdx.x == 0) s[(int64_t(e) * gridDim.y + nb) * gridDim.x + kb] = sc;
+    if (!TURN) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint2 b = make_uint2(pack4_e4m3(v[i], div), pack4_e4m3(v[i] + 4, div));
-        if (!TURN) {
-            const int r = r0 + ry + 16 * i, c = c0 + cx;
-            if (r < rows && c < cols) *reinterpret_cast<uint2*>(q + base + int64_t(r) * K + c) = b;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                turn[(cx + j) * kTurnPitch + ry + 16 * i] = uint8_t((j < 4 ? b.x >> (8 * j) : b.y >> (8 * (j - 4))) & 0xFFu);
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + ry + i, c = c0 + cx;
+            if (r < rows && c < cols)
+                *reinterpret_cast<uint2*>(q + base + int64_t(r) * K + c) =
+                    make_uint2(pack4_e4m3(v[i], div), pack4_e4m3(v[i] + 4, div));
         }
-    }
-    if (TURN) {
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
+            const int n = cx + j;
+            *reinterpret_cast<uint2*>(turn + n * 128 + (((ry >> 3) ^ ((n >> 3) & 15)) << 3)) =
+                make_uint2(pack4_e4m3(a, div), pack4_e4m3(a + 4, div));
+        }
         __syncthreads();
         // 16 bytes of K of one column of N a thread and step
         for (int i = threadIdx.x; i < 128 * 8; i += 256) {
-            const int n = i >> 3, k = (i & 7) * 16;
+            const int n = i >> 3, k = (i & 7) * 16, x = (n >> 3) & 15;
             if (c0 + n >= N || r0 + k >= K) continue;  // K is a multiple of 16
-            const uint32_t* p = reinterpret_cast<const uint32_t*>(turn + n * kTurnPitch + k);
-            *reinterpret_cast<uint4*>(q + base + int64_t(c0 + n) * K + r0 + k) = make_uint4(p[0], p[1], p[2], p[3]);
+            const uint2 lo = *reinterpret_cast<const uint2*>(turn + n * 128 + (((k >> 3) ^ x) << 3));
+            const uint2 hi = *reinterpret_cast<const uint2*>(turn + n * 128 + ((((k >> 3) + 1) ^ x) << 3));
+            *reinterpret_cast<uint4*>(q + base + int64_t(c0 + n) * K + r0 + k) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         }
     }
 }
@@ -148,7 +198,8 @@ extern "C" {
 int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int64_t ld_x, int64_t src_rows,
                     const int32_t* row_index, const int32_t* n_rows, uint8_t* q, float* s, void* ws, size_t ws_bytes,
                     moe_stream_t stream) {
-    if (rows < 0 || rows >= (int64_t(1) << 31) || K < 16 || K % 16 || src_rows < 0) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || rows >= (int64_t(1) << 31) || K < 16 || K % 16 || src_rows < 0 || K > MOE_F8_MAX_K)
+        return MOE_ERR_INVALID_ARG;
     if (x_dtype < MOE_DT_F32 || x_dtype > MOE_DT_F16) return MOE_ERR_INVALID_ARG;
     if (ld_x != 0 && (ld_x < K || ld_x > (int64_t(1) << 31))) return MOE_ERR_INVALID_ARG;
     if (!row_index && src_rows < rows) return MOE_ERR_INVALID_ARG;
@@ -162,20 +213,23 @@ int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int
     if (!aligned(q, 16) || !aligned(s, 4) || !aligned(x, es) || !aligned(row_index, 4) || !aligned(n_rows, 4))
         return MOE_ERR_MISALIGNED;
     const bool vec = aligned(x, 4 * es) && ld % 4 == 0;
-    const int64_t chunks = (K + 32 * 8 * kRowNV - 1) / (32 * 8 * kRowNV);
-    const int64_t blocks = std::min<int64_t>((rows * chunks + 7) / 8, int64_t(num_sms()) * 8);
+    // 8 rows a warp once that gives every scheduler of every SM four warps
+    const bool many = rows >= int64_t(num_sms()) * 16 * 8;
+    const int64_t units = many ? (rows + 7) / 8 : rows;
+    const dim3 grid(int(std::min<int64_t>((units + 7) / 8, int64_t(num_sms()) * 8)), many ? 1 : (K + kChunk - 1) / kChunk);
     ProfScope prof_(MOE_K_QUANT_F8, stream);
-    const cudaError_t e =
-        vec ? launch_pdl(use_pdl(rows), quantize_rows_kernel<true>, dim3(int(blocks)), dim3(256), 0, stream, x, x_dtype,
-                         ld, src_rows, row_index, n_rows, rows, K, q, s, static_cast<uint32_t*>(ws))
-            : launch_pdl(use_pdl(rows), quantize_rows_kernel<false>, dim3(int(blocks)), dim3(256), 0, stream, x,
-                         x_dtype, ld, src_rows, row_index, n_rows, rows, K, q, s, static_cast<uint32_t*>(ws));
+    auto go = [&](auto kernel) {
+        return launch_pdl(use_pdl(rows), kernel, grid, dim3(256), 0, stream, x, x_dtype, ld, src_rows, row_index, n_rows,
+                          int(rows), K, q, s, static_cast<uint32_t*>(ws));
+    };
+    const cudaError_t e = many ? (vec ? go(quantize_rows_kernel<true, 8>) : go(quantize_rows_kernel<false, 8>))
+                               : (vec ? go(quantize_rows_kernel<true, 1>) : go(quantize_rows_kernel<false, 1>));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 int moe_quantize_f8_weights(int32_t E, int32_t N, int32_t K, const void* w, int32_t w_dtype, int32_t transposed,
                             uint8_t* q, float* s, moe_stream_t stream) {
-    if (E < 1 || E > 65535 || N < 8 || N % 8 || K < 16 || K % 16 || (transposed != 0 && transposed != 1))
+    if (E < 1 || E > 65535 || N < 8 || N % 8 || K < 16 || K % 16 || K > MOE_F8_MAX_K || (transposed != 0 && transposed != 1))
         return MOE_ERR_INVALID_ARG;
     if (w_dtype < MOE_DT_F32 || w_dtype > MOE_DT_F16) return MOE_ERR_INVALID_ARG;
     if ((N + 127) / 128 > 65535 || int64_t(N) * K >= (int64_t(1) << 40)) return MOE_ERR_INVALID_ARG;

@@ -177,14 +177,14 @@ MOE_DEV bool in_row(int i, int j, int d, int th, int t) {
     return quad_in<L>(quad_at(i, j >> 2, th, t), d);
 }
 
-// ---- rows on their way through shared memory (vector layouts). Each thread copies the quads that
-// it will read itself, so nothing but its own wait for them is needed; quad q of the block's thread t
-// sits at q * threads + t. Room for a row of a tensor: stage_pieces() * 16 bytes a thread.
+// ---- rows on their way through shared memory (vector layouts, every row on 16 bytes). Quad q of
+// the block's thread t sits at q * threads + t. A warp copies its own quads in 16-byte pieces: of
+// fp32 a quad a lane, of 16 bits two quads of neighbouring lanes (8-byte copies of the lane's own
+// took a third longer). So a warp's copies are its own affair: each lane waits for its pieces, the
+// warp meets, and meets again before the place is copied to anew. Room for a row of a tensor:
+// stage_pieces() * 16 bytes a thread.
 __host__ __device__ inline int stage_pieces(int nv, int dt) { return nv * (dt == MOE_DT_F32 ? 2 : 1); }
 
-MOE_DEV void cp_async_8(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
 // base: the tensor's place in the stage (thread 0's).
 template <int NV, int L, int THREADS>
 MOE_DEV void copy_row(uint32_t base, const char* row, int d, int dt, int th, int t) {
@@ -195,10 +195,14 @@ MOE_DEV void copy_row(uint32_t base, const char* row, int d, int dt, int th, int
             if (quad_in<L>(c, d)) cp_async_16(base + (q * THREADS + threadIdx.x) * 16, row + c * 4, 16);
         }
     } else {
+        const int lane = t & 31;
 #pragma unroll
-        for (int q = 0; q < 2 * NV; ++q) {
-            const int c = (q * th + t) * 4;
-            if (quad_in<L>(c, d)) cp_async_8(base + (q * THREADS + threadIdx.x) * 8, row + c * 2);
+        for (int i = 0; i < NV; ++i) {
+            const int q = 2 * i + (lane >> 4);  // half a warp a quad row: 16 pieces of 8 elements
+            const int c = (q * th + (t & ~31)) * 4 + (lane & 15) * 8;
+            if (quad_in<L>(c, d))
+                cp_async_16(base + (q * THREADS + (threadIdx.x & ~31)) * 8 + (lane & 15) * 16, row + c * 2,
+                            L == kFullRow || c + 8 <= d ? 16 : 8);  // d may end after half a piece
         }
     }
 }

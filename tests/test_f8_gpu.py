@@ -90,6 +90,31 @@ def test_rows_gathered_with_a_row_count():
     assert (bits(q)[~keep] == 77).all() and (s.cpu().numpy()[:, ~keep] == -5).all()
 
 
+@pytest.mark.parametrize("R,K,n,bad", [(19001, 144, 19001, []), (19000, 4240, 18997, []), (18950, 1040, 18950, [0, 9, 18949]),
+                                       (20000, 128, 3, [])])
+def test_many_rows(R, K, n, bad):
+    """Enough rows for a warp to take eight of them; a last group of fewer, left rows, bad indices."""
+    rng = np.random.default_rng([R, K])
+    x = torch.from_numpy(rng.normal(0, 1, (61, K)).astype(np.float32)).cuda().bfloat16()
+    idx = rng.integers(0, 61, R).astype(np.int32)
+    for i in bad:
+        idx[i] = 61
+    q, s = torch.full((R, K), 77, dtype=torch.uint8, device="cuda"), torch.full(((K + 127) // 128, R), -5.0, device="cuda")
+    ws = ws256()
+    b.quantize_f8(x, q, s, ws, row_index=torch.from_numpy(idx).cuda(), n_rows=torch.tensor([n], dtype=torch.int32, device="cuda"))
+    assert b.get_error(ws) == (b.DEVERR_BOUNDS if bad else 0)
+    one, so = torch.empty(61, K, dtype=torch.uint8, device="cuda"), torch.empty((K + 127) // 128, 61, device="cuda")
+    b.quantize_f8(x, one, so, ws256())
+    rq, rs = o.quantize_rows(x.float().cpu().numpy())
+    assert np.array_equal(so.cpu().numpy(), rs) and np.array_equal(o.e4m3_values(bits(one)), rq)
+    keep = np.ones(R, bool)
+    keep[n:] = False
+    keep[bad] = False
+    want_q, want_s = bits(one)[np.minimum(idx, 60)], so.cpu().numpy()[:, np.minimum(idx, 60)]
+    want_q[~keep], want_s[:, ~keep] = 77, -5
+    assert np.array_equal(bits(q), want_q) and np.array_equal(s.cpu().numpy(), want_s)
+
+
 def test_infinities_and_nan_make_their_block_nan():
     x = torch.randn(3, 256, device="cuda")
     x[0, 3], x[1, 200] = float("inf"), float("nan")
