@@ -17,21 +17,6 @@ namespace {
 
 constexpr int kRowNV = 4;  // groups of 8 columns a lane: 1024 columns a warp
 
-template <bool VEC>
-MOE_DEV void load8(float (&v)[8], const void* p, int64_t i, int dt) {
-    if (!VEC) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = load_elem(p, i + j, dt);
-    } else if (dt == MOE_DT_F32) {
-        const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-        const float4 a = q[0], b = q[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), dt == MOE_DT_BF16, v);
-    }
-}
-
 // RPW: rows a warp. 8 (many rows): their scales of a block of columns lie next to each other and
 // leave as whole sectors, where one row a warp writes 4 bytes of a sector at a time, as many of those
 // as there are 128-byte pieces of q. 1 (few rows): a warp takes 1024 columns of a row.
@@ -90,16 +75,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int x
                                 v[k][j] = cc < dc ? load_elem(p, cc + (j & 3), x_dt) : 0.f;  // K is a multiple of 16
                             }
                     }
-                    uint8_t* qr = q + int64_t(r0 + i) * K + c;
-#pragma unroll
-                    for (int k = 0; k < 2 * kRowNV; ++k) {
-                        const float* w = v[k >> 1] + 4 * (k & 1);
-                        const uint32_t m = max(max(abs_bits(w[0]), abs_bits(w[1])), max(abs_bits(w[2]), abs_bits(w[3])));
-                        const F8Div div(f8_scale(__reduce_max_sync(0xFFFFFFFFu, m)));
-                        const int cc = (k * 32 + lane) * 4;
-                        if (cc < dc) *reinterpret_cast<uint32_t*>(qr + cc) = pack4_e4m3(w, div);
-                        if (lane == ((c - c0) >> 7) + k) sc[i] = div.s;
-                    }
+                    // lane k of this chunk's 2 kRowNV scales goes to lane (c - c0) / 128 + k of the span's
+                    const float got = round_row_e4m3<kRowNV, kVecRow>(v, q + int64_t(r0 + i) * K + c, dc, 32, lane);
+                    const int first = (c - c0) >> 7;
+                    const float moved = __shfl_sync(0xFFFFFFFFu, got, (lane - first) & 31);
+                    if (lane >= first && lane < first + 2 * kRowNV) sc[i] = moved;
                 }
             }
             const int g = c0 / 128 + lane;
@@ -124,9 +104,22 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int x
 // a thread's 8 values along K of a column are 8 neighbouring bytes of it, rounded two at a time along
 // K, and pass through shared memory: chunk c of column n's 128 bytes at n*128 + 8 (c ^ n/8 % 16), so
 // that a half warp's writes, eight columns apart, fall in all the banks.
-template <bool VEC, bool TURN>
-__global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, int w_dt, int N, int K, uint8_t* q,
-                                                               float* s) {
+// The values stay in registers as they were read (F32: 8 words a row, else 4) between the block's
+// largest magnitude and their rounding.
+template <bool F32>
+MOE_DEV void widen(const uint4 (&r)[F32 ? 2 : 1], bool bf16, float (&v)[8]) {
+    if (F32) {
+        const uint4 a = r[0], b = r[F32 ? 1 : 0];
+        v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+    } else {
+        unpack8(r[0], bf16, v);
+    }
+}
+
+template <bool VEC, bool TURN, bool F32>
+__global__ void __launch_bounds__(256, F32 ? 2 : 4) quantize_weights_kernel(const void* w, int w_dt, int N, int K,
+                                                                            uint8_t* q, float* s) {
     __shared__ uint32_t wmax[8];
     __shared__ __align__(16) uint8_t turn[TURN ? 128 * 128 : 16];
     griddep_wait();
@@ -136,51 +129,84 @@ __global__ void __launch_bounds__(256) quantize_weights_kernel(const void* w, in
     const int r0 = (TURN ? kb : nb) * 128, c0 = (TURN ? nb : kb) * 128;
     const int cx = (threadIdx.x & 15) * 8, ry = (threadIdx.x >> 4) * 8;
     const int64_t base = int64_t(e) * N * K;
-    float v[8][8];
-    uint32_t m = 0;
+    const bool bf16 = w_dt == MOE_DT_BF16;
+    uint4 raw[8][F32 ? 2 : 1];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int r = r0 + ry + i, c = c0 + cx;
+        const int64_t at = base + int64_t(r) * cols + c;
+        const bool in = r < rows && c < cols;  // cols: a multiple of 8
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        if (r < rows && c < cols) load8<VEC>(v[i], w, base + int64_t(r) * cols + c, w_dt);  // cols: a multiple of 8
+        for (int h = 0; h < (F32 ? 2 : 1); ++h) {
+            raw[i][h] = make_uint4(0, 0, 0, 0);
+            if (!in) continue;
+            if (VEC) {
+                raw[i][h] = F32 ? *reinterpret_cast<const uint4*>(static_cast<const float*>(w) + at + 4 * h)
+                                : *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + at);
+            } else if (F32) {
+                const uint32_t* p = static_cast<const uint32_t*>(w) + at + 4 * h;
+                raw[i][h] = make_uint4(p[0], p[1], p[2], p[3]);
+            } else {
+                const uint16_t* p = static_cast<const uint16_t*>(w) + at;
+                raw[i][h] = make_uint4(p[0] | uint32_t(p[1]) << 16, p[2] | uint32_t(p[3]) << 16, p[4] | uint32_t(p[5]) << 16,
+                                       p[6] | uint32_t(p[7]) << 16);
+            }
+        }
     }
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        float v[8];
+        widen<F32>(raw[i], bf16, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[i][j]));
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(v[j]));
+    }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     if ((threadIdx.x & 31) == 0) wmax[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, wmax[i]);
-    const float sc = f8_scale(m);
-    const F8Div div(sc);
-    if (threadIdx.x == 0) s[(int64_t(e) * gridDim.y + nb) * gridDim.x + kb] = sc;
+    const F8Div div(f8_scale(m));
+    if (threadIdx.x == 0) s[(int64_t(e) * gridDim.y + nb) * gridDim.x + kb] = div.s;
     if (!TURN) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int r = r0 + ry + i, c = c0 + cx;
+            float v[8];
+            widen<F32>(raw[i], bf16, v);
             if (r < rows && c < cols)
-                *reinterpret_cast<uint2*>(q + base + int64_t(r) * K + c) =
-                    make_uint2(pack4_e4m3(v[i], div), pack4_e4m3(v[i] + 4, div));
+                *reinterpret_cast<uint2*>(q + base + int64_t(r) * K + c) = make_uint2(pack4_e4m3(v, div), pack4_e4m3(v + 4, div));
         }
     } else {
+        // two rows' bytes of each column at a time, then 8 rows' bytes of a column
+        uint32_t lo[8], hi[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) lo[j] = hi[j] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            float a[8], b[8];
+            widen<F32>(raw[i], bf16, a);
+            widen<F32>(raw[i + 1], bf16, b);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t two = div.fast ? pack_e4m3x2(div(a[j]), div(b[j])) : pack_e4m3x2(__fdiv_rn(a[j], div.s), __fdiv_rn(b[j], div.s));
+                if (i < 4) lo[j] |= two << (8 * i);
+                else hi[j] |= two << (8 * (i - 4));
+            }
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float a[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
             const int n = cx + j;
-            *reinterpret_cast<uint2*>(turn + n * 128 + (((ry >> 3) ^ ((n >> 3) & 15)) << 3)) =
-                make_uint2(pack4_e4m3(a, div), pack4_e4m3(a + 4, div));
+            *reinterpret_cast<uint2*>(turn + n * 128 + (((ry >> 3) ^ ((n >> 3) & 15)) << 3)) = make_uint2(lo[j], hi[j]);
         }
         __syncthreads();
         // 16 bytes of K of one column of N a thread and step
         for (int i = threadIdx.x; i < 128 * 8; i += 256) {
             const int n = i >> 3, k = (i & 7) * 16, x = (n >> 3) & 15;
             if (c0 + n >= N || r0 + k >= K) continue;  // K is a multiple of 16
-            const uint2 lo = *reinterpret_cast<const uint2*>(turn + n * 128 + (((k >> 3) ^ x) << 3));
-            const uint2 hi = *reinterpret_cast<const uint2*>(turn + n * 128 + ((((k >> 3) + 1) ^ x) << 3));
-            *reinterpret_cast<uint4*>(q + base + int64_t(c0 + n) * K + r0 + k) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            const uint2 p = *reinterpret_cast<const uint2*>(turn + n * 128 + (((k >> 3) ^ x) << 3));
+            const uint2 p2 = *reinterpret_cast<const uint2*>(turn + n * 128 + ((((k >> 3) + 1) ^ x) << 3));
+            *reinterpret_cast<uint4*>(q + base + int64_t(c0 + n) * K + r0 + k) = make_uint4(p.x, p.y, p2.x, p2.y);
         }
     }
 }
@@ -242,8 +268,13 @@ int moe_quantize_f8_weights(int32_t E, int32_t N, int32_t K, const void* w, int3
     auto go = [&](auto kernel) {
         return launch_pdl(false, kernel, grid, dim3(256), 0, stream, w, w_dtype, N, K, q, s);
     };
-    const cudaError_t e = transposed ? (vec ? go(quantize_weights_kernel<true, true>) : go(quantize_weights_kernel<false, true>))
-                                     : (vec ? go(quantize_weights_kernel<true, false>) : go(quantize_weights_kernel<false, false>));
+    cudaError_t e;
+    if (w_dtype == MOE_DT_F32)
+        e = transposed ? (vec ? go(quantize_weights_kernel<true, true, true>) : go(quantize_weights_kernel<false, true, true>))
+                       : (vec ? go(quantize_weights_kernel<true, false, true>) : go(quantize_weights_kernel<false, false, true>));
+    else
+        e = transposed ? (vec ? go(quantize_weights_kernel<true, true, false>) : go(quantize_weights_kernel<false, true, false>))
+                       : (vec ? go(quantize_weights_kernel<true, false, false>) : go(quantize_weights_kernel<false, false, false>));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

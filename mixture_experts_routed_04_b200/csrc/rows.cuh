@@ -265,6 +265,7 @@ MOE_DEV uint32_t pack_e4m3x2(float lo, float hi) {
 struct F8Div {
     float s, rs;
     bool fast;
+    F8Div() = default;
     MOE_DEV explicit F8Div(float scale) {
         s = scale;
         rs = __fdiv_rn(1.0f, scale);
@@ -282,23 +283,60 @@ MOE_DEV uint32_t pack4_e4m3(const float* v, const F8Div& div) {
                           pack_e4m3x2(__fdiv_rn(v[2], div.s), __fdiv_rn(v[3], div.s)) << 16;
 }
 
-// A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes;
-// s: scale of column group 0, the next ones `lds` on. Every thread of the warp takes part.
+// The scales of a warp's N <= 32 groups of 128 columns from their largest magnitudes m[k], which the
+// warp agrees on: lane k divides for group k, so that the two divisions are done once a warp and not
+// once a lane and group. Warp-uniform result: whether every group's quotients may take the short way.
+template <int N>
+MOE_DEV bool warp_scales(const uint32_t (&m)[N], float& scale, float& recip) {
+    uint32_t mine = 0;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if ((threadIdx.x & 31) == k) mine = m[k];
+    const F8Div div(f8_scale(mine));
+    scale = div.s;
+    recip = div.rs;
+    return __all_sync(0xFFFFFFFFu, div.fast || (threadIdx.x & 31) >= N);
+}
+
+// A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes.
+// Lane k gets the scale of the warp's k-th quad row. Every thread of the warp takes part.
+template <int NV, int L>
+MOE_DEV float round_row_e4m3(const float (&v)[NV][8], uint8_t* q, int d, int th, int t) {
+    uint32_t m[2 * NV];
+#pragma unroll
+    for (int k = 0; k < 2 * NV; ++k) {
+        const float* x = v[k >> 1] + 4 * (k & 1);
+        m[k] = __reduce_max_sync(0xFFFFFFFFu, max(max(abs_bits(x[0]), abs_bits(x[1])), max(abs_bits(x[2]), abs_bits(x[3]))));
+    }
+    float scale, recip;
+    const bool fast = warp_scales(m, scale, recip);
+#pragma unroll
+    for (int k = 0; k < 2 * NV; ++k) {
+        F8Div div;
+        div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
+        div.rs = __shfl_sync(0xFFFFFFFFu, recip, k);
+        div.fast = true;
+        const int c = (k * th + t) * 4;
+        if (fast && quad_in<L>(c, d)) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v[k >> 1] + 4 * (k & 1), div);
+    }
+    if (!fast) {  // a tiny, infinite or NaN scale among them: divide
+#pragma unroll
+        for (int k = 0; k < 2 * NV; ++k) {
+            F8Div div;
+            div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
+            div.fast = false;
+            const int c = (k * th + t) * 4;
+            if (quad_in<L>(c, d)) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v[k >> 1] + 4 * (k & 1), div);
+        }
+    }
+    return scale;
+}
+// The same with the scales: s is that of column group 0, the next ones `lds` on.
 template <int NV, int L>
 MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64_t lds, int d, int th, int t) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float* x = v[i] + 4 * h;
-            const uint32_t m = max(max(abs_bits(x[0]), abs_bits(x[1])), max(abs_bits(x[2]), abs_bits(x[3])));
-            const F8Div div(f8_scale(__reduce_max_sync(0xFFFFFFFFu, m)));
-            const int c = quad_at(i, h, th, t);
-            if (quad_in<L>(c, d)) {
-                *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(x, div);
-                if ((t & 31) == 0) s[int64_t(c >> 7) * lds] = div.s;
-            }
-        }
+    const float scale = round_row_e4m3<NV, L>(v, q, d, th, t);
+    const int lane = t & 31, c = (lane * th + (t & ~31)) * 4;  // lane k: the first column of the warp's k-th quad row
+    if (lane < 2 * NV && quad_in<L>(c, d)) s[int64_t(c >> 7) * lds] = scale;
 }
 
 }  // namespace moe
