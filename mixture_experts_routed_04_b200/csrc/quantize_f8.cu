@@ -15,27 +15,103 @@ namespace moe {
 
 namespace {
 
-constexpr int kRowNV = 4;  // groups of 8 columns a lane: 1024 columns a warp
+constexpr int kQuads = 8;                // quads a lane: a warp holds 1024 columns at once
+constexpr int kChunk = 32 * 4 * kQuads;
+constexpr int kSpan = 32 * 128;          // columns whose scales a warp gathers, one a lane
+
+// Rounds columns c0 .. c0 + dc (<= kChunk) of a row; scales[k]: of the k-th 128 of them. The values stay
+// as they were read (a third of the registers of fp32 copies of bf16) between the groups' largest
+// magnitudes and their rounding.
+template <bool VEC, bool F32>
+MOE_DEV void round_chunk(const char* p, int dc, bool bf16, uint8_t* q, float* scales, int lane) {
+    uint4 raw[F32 ? kQuads : kQuads / 2];
+    auto quad = [&](int k, float* v) {
+        if (F32) {
+            const uint4 a = raw[k];
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+            v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+        } else {
+            const uint4 a = raw[k >> 1];
+            unpack4(k & 1 ? make_uint2(a.z, a.w) : make_uint2(a.x, a.y), bf16, v);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+        const int c = (k * 32 + lane) * 4;
+        uint4 a = make_uint4(0, 0, 0, 0);
+        if (c < dc) {  // K is a multiple of 16
+            if (F32) {
+                const uint32_t* x = reinterpret_cast<const uint32_t*>(p) + c;
+                a = VEC ? *reinterpret_cast<const uint4*>(x) : make_uint4(x[0], x[1], x[2], x[3]);
+            } else {
+                const uint16_t* x = reinterpret_cast<const uint16_t*>(p) + c;
+                const uint2 h = VEC ? *reinterpret_cast<const uint2*>(x)
+                                    : make_uint2(x[0] | uint32_t(x[1]) << 16, x[2] | uint32_t(x[3]) << 16);
+                a.x = h.x;
+                a.y = h.y;
+            }
+        }
+        if (F32) {
+            raw[k] = a;
+        } else if (k & 1) {
+            raw[k >> 1].z = a.x;
+            raw[k >> 1].w = a.y;
+        } else {
+            raw[k >> 1].x = a.x;
+            raw[k >> 1].y = a.y;
+        }
+    }
+    uint32_t m[kQuads];
+#pragma unroll
+    for (int k = 0; k < kQuads; ++k) {
+        float v[4];
+        quad(k, v);
+        m[k] = __reduce_max_sync(0xFFFFFFFFu, max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3]))));
+    }
+    float scale, recip;
+    const bool fast = warp_scales(m, scale, recip);
+    if (lane < kQuads) scales[lane] = scale;
+    if (fast) {
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const float s = __shfl_sync(0xFFFFFFFFu, scale, k), rs = __shfl_sync(0xFFFFFFFFu, recip, k);
+            const int c = (k * 32 + lane) * 4;
+            float v[4];
+            quad(k, v);
+            if (c < dc) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3_fast(v, s, rs);
+        }
+    } else {  // a tiny, infinite or NaN scale among them
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            F8Div div;
+            div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
+            div.fast = false;
+            const int c = (k * 32 + lane) * 4;
+            float v[4];
+            quad(k, v);
+            if (c < dc) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v, div);
+        }
+    }
+}
 
 // RPW: rows a warp. 8 (many rows): their scales of a block of columns lie next to each other and
 // leave as whole sectors, where one row a warp writes 4 bytes of a sector at a time, as many of those
-// as there are 128-byte pieces of q. 1 (few rows): a warp takes 1024 columns of a row.
-constexpr int kChunk = 32 * 8 * kRowNV;  // columns a warp holds at once
-constexpr int kSpan = 32 * 128;          // columns whose scales a warp holds, one a lane
-
-template <bool VEC, int RPW>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int x_dt, int64_t ld, int64_t src_rows,
+// as there are 128-byte pieces of q. 1 (few rows): a warp takes 1024 columns of a row (the grid's
+// second dimension).
+template <bool VEC, bool F32, int RPW>
+__global__ void __launch_bounds__(256, F32 ? 3 : 4) quantize_rows_kernel(const void* x, int x_dt, int64_t ld, int64_t src_rows,
                                                             const int32_t* row_index, const int32_t* n_rows, int rows,
                                                             int K, uint8_t* q, float* s, uint32_t* err) {
+    __shared__ float held[8][RPW][32 + 1];  // a warp's scales of a span: [row][group]
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31;
+    float(*mine)[33] = held[threadIdx.x >> 5];
     const int n = n_rows ? min(rows, max(0, *n_rows)) : rows;
-    const bool wide = (reinterpret_cast<uintptr_t>(s) & 15) == 0;
-    const int units = RPW > 1 ? (n + RPW - 1) / RPW : n;
-    const int warps = gridDim.x * (blockDim.x >> 5);
+    const bool wide = (reinterpret_cast<uintptr_t>(s) & 15) == 0 && rows % 4 == 0, bf16 = x_dt == MOE_DT_BF16;
+    const int units = (n + RPW - 1) / RPW, warps = gridDim.x * (blockDim.x >> 5);
+    const int first = RPW > 1 ? 0 : int(blockIdx.y) * kChunk, last = RPW > 1 ? K : min(K, first + kChunk);
     bool bad = false;
-    // RPW 1: the grid's second dimension is the chunk of columns
     for (int64_t u = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < units; u += warps) {
         const int r0 = int(u) * RPW, nr = min(RPW, n - r0);
         int src = -1;
@@ -50,50 +126,31 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void* x, int x
             }
         }
         const uint32_t ok = __ballot_sync(0xFFFFFFFFu, src >= 0);  // rows to write
-        for (int c0 = RPW > 1 ? 0 : int(blockIdx.y) * kChunk; c0 < (RPW > 1 ? K : min(K, int(blockIdx.y + 1) * kChunk));
-             c0 += kSpan) {
-            float sc[RPW];  // lane: group of columns c0 / 128 + lane
-#pragma unroll
+        for (int c0 = first; c0 < last; c0 += kSpan) {
+            const int end = min(last, c0 + kSpan);
+#pragma unroll 1
             for (int i = 0; i < RPW; ++i) {
-                sc[i] = 0.f;
                 const int row = __shfl_sync(0xFFFFFFFFu, src, i);
                 if (row < 0) continue;
-                const int end = RPW > 1 ? min(K, c0 + kSpan) : min(K, c0 + kChunk);
-                for (int c = c0; c < end; c += kChunk) {
-                    float v[kRowNV][8];
-                    const int dc = min(end - c, kChunk);
-                    const char* p = static_cast<const char*>(x) + (row * ld + c) * (x_dt == MOE_DT_F32 ? 4 : 2);
-                    if (VEC) {
-                        if (dc == kChunk) load_row<kRowNV, kFullRow>(v, p, dc, x_dt, 32, lane);
-                        else load_row<kRowNV, kVecRow>(v, p, dc, x_dt, 32, lane);
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < kRowNV; ++k)
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int cc = quad_at(k, j >> 2, 32, lane);
-                                v[k][j] = cc < dc ? load_elem(p, cc + (j & 3), x_dt) : 0.f;  // K is a multiple of 16
-                            }
-                    }
-                    // lane k of this chunk's 2 kRowNV scales goes to lane (c - c0) / 128 + k of the span's
-                    const float got = round_row_e4m3<kRowNV, kVecRow>(v, q + int64_t(r0 + i) * K + c, dc, 32, lane);
-                    const int first = (c - c0) >> 7;
-                    const float moved = __shfl_sync(0xFFFFFFFFu, got, (lane - first) & 31);
-                    if (lane >= first && lane < first + 2 * kRowNV) sc[i] = moved;
-                }
+#pragma unroll 1
+                for (int c = c0; c < end; c += kChunk)
+                    round_chunk<VEC, F32>(static_cast<const char*>(x) + (row * ld + c) * (F32 ? 4 : 2), min(end - c, kChunk),
+                                          bf16, q + int64_t(r0 + i) * K + c, mine[i] + ((c - c0) >> 7), lane);
             }
+            __syncwarp();
             const int g = c0 / 128 + lane;
-            if (g * 128 < K && (RPW > 1 || lane < kChunk / 128)) {
+            if (g * 128 < last) {
                 float* sp = s + int64_t(g) * rows + r0;
-                if (RPW == 8 && ok == 0xFFu && rows % 4 == 0 && wide) {
-                    reinterpret_cast<float4*>(sp)[0] = make_float4(sc[0], sc[1 % RPW], sc[2 % RPW], sc[3 % RPW]);
-                    reinterpret_cast<float4*>(sp)[1] = make_float4(sc[4 % RPW], sc[5 % RPW], sc[6 % RPW], sc[7 % RPW]);
+                if (RPW == 8 && ok == 0xFFu && wide) {
+                    reinterpret_cast<float4*>(sp)[0] = make_float4(mine[0][lane], mine[1 % RPW][lane], mine[2 % RPW][lane], mine[3 % RPW][lane]);
+                    reinterpret_cast<float4*>(sp)[1] = make_float4(mine[4 % RPW][lane], mine[5 % RPW][lane], mine[6 % RPW][lane], mine[7 % RPW][lane]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < RPW; ++i)
-                        if (ok >> i & 1u) sp[i] = sc[i];
+                        if (ok >> i & 1u) sp[i] = mine[i][lane];
                 }
             }
+            __syncwarp();
         }
     }
     if (bad) set_error(err, MOE_DEVERR_BOUNDS);
@@ -248,8 +305,13 @@ int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int
         return launch_pdl(use_pdl(rows), kernel, grid, dim3(256), 0, stream, x, x_dtype, ld, src_rows, row_index, n_rows,
                           int(rows), K, q, s, static_cast<uint32_t*>(ws));
     };
-    const cudaError_t e = many ? (vec ? go(quantize_rows_kernel<true, 8>) : go(quantize_rows_kernel<false, 8>))
-                               : (vec ? go(quantize_rows_kernel<true, 1>) : go(quantize_rows_kernel<false, 1>));
+    cudaError_t e;
+    if (x_dtype == MOE_DT_F32)
+        e = many ? (vec ? go(quantize_rows_kernel<true, true, 8>) : go(quantize_rows_kernel<false, true, 8>))
+                 : (vec ? go(quantize_rows_kernel<true, true, 1>) : go(quantize_rows_kernel<false, true, 1>));
+    else
+        e = many ? (vec ? go(quantize_rows_kernel<true, false, 8>) : go(quantize_rows_kernel<false, false, 8>))
+                 : (vec ? go(quantize_rows_kernel<true, false, 1>) : go(quantize_rows_kernel<false, false, 1>));
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

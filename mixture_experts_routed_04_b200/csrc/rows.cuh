@@ -276,9 +276,21 @@ struct F8Div {
         return fmaf(-fmaf(q, s, -x), rs, q);  // the remainder with this sign keeps -0
     }
 };
-// Four values of a group whose scale is s.
+// Four values of a group whose scale is s; two quotients an instruction.
+MOE_DEV uint32_t pack4_e4m3_fast(const float* v, float s, float rs) {
+    const float2 s2 = make_float2(s, s), r2 = make_float2(rs, rs), n2 = make_float2(-rs, -rs);
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
+        const float2 q = __fmul2_rn(x, r2);
+        const float2 y = __ffma2_rn(__ffma2_rn(q, s2, make_float2(-x.x, -x.y)), n2, q);
+        w[i] = pack_e4m3x2(y.x, y.y);
+    }
+    return w[0] | w[1] << 16;
+}
 MOE_DEV uint32_t pack4_e4m3(const float* v, const F8Div& div) {
-    return div.fast ? pack_e4m3x2(div(v[0]), div(v[1])) | pack_e4m3x2(div(v[2]), div(v[3])) << 16
+    return div.fast ? pack4_e4m3_fast(v, div.s, div.rs)
                     : pack_e4m3x2(__fdiv_rn(v[0], div.s), __fdiv_rn(v[1], div.s)) |
                           pack_e4m3x2(__fdiv_rn(v[2], div.s), __fdiv_rn(v[3], div.s)) << 16;
 }
@@ -298,10 +310,10 @@ MOE_DEV bool warp_scales(const uint32_t (&m)[N], float& scale, float& recip) {
     return __all_sync(0xFFFFFFFFu, div.fast || (threadIdx.x & 31) >= N);
 }
 
-// A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes.
-// Lane k gets the scale of the warp's k-th quad row. Every thread of the warp takes part.
+// A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes;
+// s: scale of column group 0, the next ones `lds` on. Every thread of the warp takes part.
 template <int NV, int L>
-MOE_DEV float round_row_e4m3(const float (&v)[NV][8], uint8_t* q, int d, int th, int t) {
+MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64_t lds, int d, int th, int t) {
     uint32_t m[2 * NV];
 #pragma unroll
     for (int k = 0; k < 2 * NV; ++k) {
@@ -315,26 +327,10 @@ MOE_DEV float round_row_e4m3(const float (&v)[NV][8], uint8_t* q, int d, int th,
         F8Div div;
         div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
         div.rs = __shfl_sync(0xFFFFFFFFu, recip, k);
-        div.fast = true;
+        div.fast = fast;
         const int c = (k * th + t) * 4;
-        if (fast && quad_in<L>(c, d)) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v[k >> 1] + 4 * (k & 1), div);
+        if (quad_in<L>(c, d)) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v[k >> 1] + 4 * (k & 1), div);
     }
-    if (!fast) {  // a tiny, infinite or NaN scale among them: divide
-#pragma unroll
-        for (int k = 0; k < 2 * NV; ++k) {
-            F8Div div;
-            div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
-            div.fast = false;
-            const int c = (k * th + t) * 4;
-            if (quad_in<L>(c, d)) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v[k >> 1] + 4 * (k & 1), div);
-        }
-    }
-    return scale;
-}
-// The same with the scales: s is that of column group 0, the next ones `lds` on.
-template <int NV, int L>
-MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64_t lds, int d, int th, int t) {
-    const float scale = round_row_e4m3<NV, L>(v, q, d, th, t);
     const int lane = t & 31, c = (lane * th + (t & ~31)) * 4;  // lane k: the first column of the warp's k-th quad row
     if (lane < 2 * NV && quad_in<L>(c, d)) s[int64_t(c >> 7) * lds] = scale;
 }
