@@ -22,8 +22,10 @@ constexpr int kSpan = 32 * 128;          // columns whose scales a warp gathers,
 // Rounds columns c0 .. c0 + dc (<= kChunk) of a row; scales[k]: of the k-th 128 of them. The values stay
 // as they were read (a third of the registers of fp32 copies of bf16) between the groups' largest
 // magnitudes and their rounding.
-template <bool VEC, bool F32>
-MOE_DEV void round_chunk(const char* p, int dc, bool bf16, uint8_t* q, float* scales, int lane) {
+// FULL: dc is kChunk.
+template <bool VEC, int DT, bool FULL>
+MOE_DEV void round_chunk(const char* p, int dc, uint8_t* q, float* scales, int lane) {
+    constexpr bool F32 = DT == MOE_DT_F32, bf16 = DT == MOE_DT_BF16;
     uint4 raw[F32 ? kQuads : kQuads / 2];
     auto quad = [&](int k, float* v) {
         if (F32) {
@@ -39,7 +41,7 @@ MOE_DEV void round_chunk(const char* p, int dc, bool bf16, uint8_t* q, float* sc
     for (int k = 0; k < kQuads; ++k) {
         const int c = (k * 32 + lane) * 4;
         uint4 a = make_uint4(0, 0, 0, 0);
-        if (c < dc) {  // K is a multiple of 16
+        if (FULL || c < dc) {  // K is a multiple of 16
             if (F32) {
                 const uint32_t* x = reinterpret_cast<const uint32_t*>(p) + c;
                 a = VEC ? *reinterpret_cast<const uint4*>(x) : make_uint4(x[0], x[1], x[2], x[3]);
@@ -66,7 +68,7 @@ MOE_DEV void round_chunk(const char* p, int dc, bool bf16, uint8_t* q, float* sc
     for (int k = 0; k < kQuads; ++k) {
         float v[4];
         quad(k, v);
-        m[k] = __reduce_max_sync(0xFFFFFFFFu, max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3]))));
+        m[k] = __reduce_max_sync(0xFFFFFFFFu, amax4_bits(v));
     }
     float scale, recip;
     const bool fast = warp_scales(m, scale, recip);
@@ -74,11 +76,11 @@ MOE_DEV void round_chunk(const char* p, int dc, bool bf16, uint8_t* q, float* sc
     if (fast) {
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
-            const float s = __shfl_sync(0xFFFFFFFFu, scale, k), rs = __shfl_sync(0xFFFFFFFFu, recip, k);
+            const float s = __shfl_sync(0xFFFFFFFFu, scale, k), nrs = __shfl_sync(0xFFFFFFFFu, -recip, k);
             const int c = (k * 32 + lane) * 4;
             float v[4];
             quad(k, v);
-            if (c < dc) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3_fast(v, s, rs);
+            if (FULL || c < dc) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3_fast(v, s, nrs);
         }
     } else {  // a tiny, infinite or NaN scale among them
 #pragma unroll
@@ -98,8 +100,8 @@ MOE_DEV void round_chunk(const char* p, int dc, bool bf16, uint8_t* q, float* sc
 // leave as whole sectors, where one row a warp writes 4 bytes of a sector at a time, as many of those
 // as there are 128-byte pieces of q. 1 (few rows): a warp takes 1024 columns of a row (the grid's
 // second dimension).
-template <bool VEC, bool F32, int RPW>
-__global__ void __launch_bounds__(256, F32 ? 3 : 4) quantize_rows_kernel(const void* x, int x_dt, int64_t ld, int64_t src_rows,
+template <bool VEC, int DT, int RPW>
+__global__ void __launch_bounds__(256, DT == MOE_DT_F32 ? 3 : 4) quantize_rows_kernel(const void* x, int64_t ld, int64_t src_rows,
                                                             const int32_t* row_index, const int32_t* n_rows, int rows,
                                                             int K, uint8_t* q, float* s, uint32_t* err) {
     __shared__ float held[8][RPW][32 + 1];  // a warp's scales of a span: [row][group]
@@ -108,7 +110,7 @@ __global__ void __launch_bounds__(256, F32 ? 3 : 4) quantize_rows_kernel(const v
     const int lane = threadIdx.x & 31;
     float(*mine)[33] = held[threadIdx.x >> 5];
     const int n = n_rows ? min(rows, max(0, *n_rows)) : rows;
-    const bool wide = (reinterpret_cast<uintptr_t>(s) & 15) == 0 && rows % 4 == 0, bf16 = x_dt == MOE_DT_BF16;
+    const bool wide = (reinterpret_cast<uintptr_t>(s) & 15) == 0 && rows % 4 == 0;
     const int units = (n + RPW - 1) / RPW, warps = gridDim.x * (blockDim.x >> 5);
     const int first = RPW > 1 ? 0 : int(blockIdx.y) * kChunk, last = RPW > 1 ? K : min(K, first + kChunk);
     bool bad = false;
@@ -133,9 +135,13 @@ __global__ void __launch_bounds__(256, F32 ? 3 : 4) quantize_rows_kernel(const v
                 const int row = __shfl_sync(0xFFFFFFFFu, src, i);
                 if (row < 0) continue;
 #pragma unroll 1
-                for (int c = c0; c < end; c += kChunk)
-                    round_chunk<VEC, F32>(static_cast<const char*>(x) + (row * ld + c) * (F32 ? 4 : 2), min(end - c, kChunk),
-                                          bf16, q + int64_t(r0 + i) * K + c, mine[i] + ((c - c0) >> 7), lane);
+                for (int c = c0; c < end; c += kChunk) {
+                    const char* p = static_cast<const char*>(x) + (row * ld + c) * (DT == MOE_DT_F32 ? 4 : 2);
+                    uint8_t* qp = q + int64_t(r0 + i) * K + c;
+                    float* sc = mine[i] + ((c - c0) >> 7);
+                    if (end - c >= kChunk) round_chunk<VEC, DT, true>(p, kChunk, qp, sc, lane);
+                    else round_chunk<VEC, DT, false>(p, end - c, qp, sc, lane);
+                }
             }
             __syncwarp();
             const int g = c0 / 128 + lane;
@@ -302,16 +308,17 @@ int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int
     const dim3 grid(int(std::min<int64_t>((units + 7) / 8, int64_t(num_sms()) * 8)), many ? 1 : (K + kChunk - 1) / kChunk);
     ProfScope prof_(MOE_K_QUANT_F8, stream);
     auto go = [&](auto kernel) {
-        return launch_pdl(use_pdl(rows), kernel, grid, dim3(256), 0, stream, x, x_dtype, ld, src_rows, row_index, n_rows,
+        return launch_pdl(use_pdl(rows), kernel, grid, dim3(256), 0, stream, x, ld, src_rows, row_index, n_rows,
                           int(rows), K, q, s, static_cast<uint32_t*>(ws));
     };
-    cudaError_t e;
-    if (x_dtype == MOE_DT_F32)
-        e = many ? (vec ? go(quantize_rows_kernel<true, true, 8>) : go(quantize_rows_kernel<false, true, 8>))
-                 : (vec ? go(quantize_rows_kernel<true, true, 1>) : go(quantize_rows_kernel<false, true, 1>));
-    else
-        e = many ? (vec ? go(quantize_rows_kernel<true, false, 8>) : go(quantize_rows_kernel<false, false, 8>))
-                 : (vec ? go(quantize_rows_kernel<true, false, 1>) : go(quantize_rows_kernel<false, false, 1>));
+    auto pick = [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        return many ? (vec ? go(quantize_rows_kernel<true, DT, 8>) : go(quantize_rows_kernel<false, DT, 8>))
+                    : (vec ? go(quantize_rows_kernel<true, DT, 1>) : go(quantize_rows_kernel<false, DT, 1>));
+    };
+    const cudaError_t e = x_dtype == MOE_DT_F32    ? pick(std::integral_constant<int, MOE_DT_F32>{})
+                          : x_dtype == MOE_DT_BF16 ? pick(std::integral_constant<int, MOE_DT_BF16>{})
+                                                   : pick(std::integral_constant<int, MOE_DT_F16>{});
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

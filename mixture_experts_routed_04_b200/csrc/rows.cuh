@@ -244,6 +244,13 @@ MOE_DEV void cp_async_wait_most(int n) {
 // infinity: a NaN or an infinity anywhere makes the scale NaN or infinite, so the
 // whole group reads back as NaN and never as plausible numbers.
 MOE_DEV uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The larger of two magnitudes; a NaN wins.
+MOE_DEV float amax2(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return m;
+}
+MOE_DEV uint32_t amax4_bits(const float* v) { return abs_bits(amax2(amax2(v[0], v[1]), amax2(v[2], v[3]))); }
 MOE_DEV float f8_scale(uint32_t amax_bits) {
     const float s = __fdiv_rn(__uint_as_float(amax_bits), 448.0f);
     return s < 1.17549435e-38f ? 1.17549435e-38f : s;  // a NaN passes
@@ -276,21 +283,23 @@ struct F8Div {
         return fmaf(-fmaf(q, s, -x), rs, q);  // the remainder with this sign keeps -0
     }
 };
-// Four values of a group whose scale is s; two quotients an instruction.
-MOE_DEV uint32_t pack4_e4m3_fast(const float* v, float s, float rs) {
-    const float2 s2 = make_float2(s, s), r2 = make_float2(rs, rs), n2 = make_float2(-rs, -rs);
+// Four values of a group whose scale is s, nrs = -1/s; two quotients an instruction. The quotient comes
+// out negative, which takes a sign off no operand of the packed fmas (they have no negation), and the
+// four signs are turned at once at the end; a zero keeps its sign.
+MOE_DEV uint32_t pack4_e4m3_fast(const float* v, float s, float nrs) {
+    const float2 s2 = make_float2(s, s), n2 = make_float2(nrs, nrs);
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const float2 x = make_float2(v[2 * i], v[2 * i + 1]);
-        const float2 q = __fmul2_rn(x, r2);
-        const float2 y = __ffma2_rn(__ffma2_rn(q, s2, make_float2(-x.x, -x.y)), n2, q);
+        const float2 q = __fmul2_rn(x, n2);                       // -x / s
+        const float2 y = __ffma2_rn(__ffma2_rn(q, s2, x), n2, q);  // less its remainder's quotient
         w[i] = pack_e4m3x2(y.x, y.y);
     }
-    return w[0] | w[1] << 16;
+    return (w[0] | w[1] << 16) ^ 0x80808080u;
 }
 MOE_DEV uint32_t pack4_e4m3(const float* v, const F8Div& div) {
-    return div.fast ? pack4_e4m3_fast(v, div.s, div.rs)
+    return div.fast ? pack4_e4m3_fast(v, div.s, -div.rs)
                     : pack_e4m3x2(__fdiv_rn(v[0], div.s), __fdiv_rn(v[1], div.s)) |
                           pack_e4m3x2(__fdiv_rn(v[2], div.s), __fdiv_rn(v[3], div.s)) << 16;
 }
@@ -318,7 +327,7 @@ MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64
 #pragma unroll
     for (int k = 0; k < 2 * NV; ++k) {
         const float* x = v[k >> 1] + 4 * (k & 1);
-        m[k] = __reduce_max_sync(0xFFFFFFFFu, max(max(abs_bits(x[0]), abs_bits(x[1])), max(abs_bits(x[2]), abs_bits(x[3]))));
+        m[k] = __reduce_max_sync(0xFFFFFFFFu, amax4_bits(x));
     }
     float scale, recip;
     const bool fast = warp_scales(m, scale, recip);
