@@ -175,15 +175,15 @@ def check(status: int, what: str = "") -> None:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()  # the prototypes make it a void*
 
 
 def _stream(stream=None):
     if stream is not None:
-        return ctypes.c_void_p(stream.cuda_stream)
+        return stream.cuda_stream
     import torch
     # the raw handle: building the Stream object of torch.cuda.current_stream() takes longer than a launch
-    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def capacity(p: Params):
@@ -378,7 +378,7 @@ def _fits(what, stream, *specs):
     if stream is not None and stream.device_index != dev:
         raise MoeError(f"{what}: the stream is not on the current device")
     for name, t, shape, dtypes, dense in specs:
-        if t is None or (t.get_device() == dev and t.shape == shape and t.dtype in dtypes and
+        if t is None or (t.shape == shape and t.dtype in dtypes and t.get_device() == dev and
                          (not dense or t.is_contiguous())):
             continue
         if t.get_device() != dev:

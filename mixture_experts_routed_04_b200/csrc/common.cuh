@@ -334,18 +334,6 @@ MOE_DEV void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)[32]) {
 }
 MOE_DEV void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
-// The same, tied to the registers that a load fills: no use of them moves before the wait.
-MOE_DEV void tmem_ld_wait(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
-                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
-                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
-                   "+r"(v[30]), "+r"(v[31])
-                 :
-                 : "memory");
-}
-
 // Shared-memory matrix descriptor (tcgen05 form, version 1), 128-byte swizzle.
 //   start: smem byte address; lbo/sbo: leading/stride byte offsets.
 // K-major SW128 operand: rows of 128 B (64 bf16 of K), 8-row groups SBO apart;

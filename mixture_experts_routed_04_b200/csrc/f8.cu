@@ -1,5 +1,7 @@
 // f8.cu — entry points of the products in 8-bit floating point: argument checks and
 // the choice between the streaming kernels (f8_stream.cu) and the tiles (f8_tile.cu).
+#include <algorithm>
+#include <cmath>
 #include <limits>
 
 #include "f8.cuh"
@@ -60,8 +62,25 @@ Args args_of(const moe_f8_params* p, const uint8_t* a, const float* a_scale, con
     return x;
 }
 
+// The streaming kernel reads an expert's weights once a chunk of 8 rows; the tiles walk K block by
+// block, each tile's blocks one after the other, however few its rows are. Estimates in us of B200
+// runs (stream / tiles): one dense product of 4096 x 4096, 8 rows 5.2 / 21.6, 32 rows 12.0 / 21.6,
+// 128 rows 39 / 24; 1024 x 1024, 128 rows 5.8 / 10.2; 768 -> 8192, 32 rows 7.7 / 7.4; 8 experts' gate
+// and up of 1536 x 4096, one row each 30.7 / 35.0, 64 experts with two rows each 220 / 145; down of
+// 4096 x 1536, 8 experts 17.8 / 16.4.
+bool takes_stream(const Args& x, bool gated) {
+    const double touched = double(std::min<int64_t>(x.rows, x.E));
+    const double chunks = x.offsets ? std::max(touched, x.rows / 8.0) : std::ceil(x.rows / 8.0);
+    const double bytes = double(x.N) * x.K * (gated ? 2 : 1), sms = num_sms();
+    const bool dense = !x.offsets;  // its chunks find the weights in L2 after the first
+    const double stream_us = 2.0 + chunks * bytes / (dense ? 6.0e6 : 3.6e6);
+    const double tiles = std::max(touched, x.rows / 128.0) * std::ceil(x.N / (gated ? 128.0 : 256.0));
+    const double tile_us = 3.0 + (dense ? 0.6 : 1.0) * x.KB * std::ceil(tiles / sms);
+    return stream_us < tile_us;
+}
+
 int launch(const moe_f8_params* p, const Args& x, bool gated, cudaStream_t s) {
-    const bool stream = p->variant == MOE_VARIANT_STREAM || (p->variant == MOE_VARIANT_AUTO && p->rows <= 16);
+    const bool stream = p->variant == MOE_VARIANT_STREAM || (p->variant == MOE_VARIANT_AUTO && takes_stream(x, gated));
     return (stream ? launch_stream(x, gated, s) : launch_tile(x, gated, s)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -56,53 +56,52 @@ MOE_DEV float row_weight(const Args& p, int64_t row) {
     return sp >= 0 ? __ldg(p.topk_w + sp) : 1.0f;
 }
 
-// Blocks of `chunk` rows of the experts, in the experts' order: block `u` is rows
-// [row0, row0 + n) of expert e; false past the last one. Every thread of a block of
-// at least 256 threads calls it (E <= 256: one expert a thread, one pass of scans;
-// a search by row would be a chain of dependent loads). sm: 12 ints.
-MOE_DEV bool find_rows(const Args& p, int u, int chunk, int* sm, int& e, int64_t& row0, int& n) {
-    if (!p.offsets) {
-        e = 0;
-        row0 = int64_t(u) * chunk;
-        n = int(min(int64_t(chunk), p.rows - row0));
-        return n > 0;
-    }
+// The experts' blocks of `chunk` rows: exclusive prefix of their numbers and the experts' row offsets.
+struct Chunks {
+    int base[kMaxE + 1];
+    int off[kMaxE + 1];
+    int warp_sum[32];
+};
+// Fills c; every thread of a block of at least 256 threads calls it (E <= 256: one expert a thread,
+// one pass of scans). Offsets outside the buffers (never from moe_permute) are reported and not
+// followed. The caller synchronises the block before it reads c.
+MOE_DEV void count_chunks(const Args& p, int chunk, Chunks& c) {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    int off = 0, cnt = 0;
-    if (t < p.E) {
-        off = __ldg(p.offsets + t);
-        cnt = __ldg(p.offsets + t + 1) - off;
-        // offsets outside the buffers (never from moe_permute) are not followed
-        if (off < 0 || cnt < 0 || int64_t(off) + cnt > p.rows) {
-            set_error(p.err, MOE_DEVERR_BOUNDS);
-            cnt = 0;
+    int cnt = 0;
+    if (!p.offsets) {
+        if (t == 0) {
+            cnt = int((p.rows + chunk - 1) / chunk);
+            c.off[0] = 0;
+            c.off[1] = int(p.rows);
         }
+    } else if (t < p.E) {
+        const int off = __ldg(p.offsets + t), end = __ldg(p.offsets + t + 1);
+        c.off[t] = off;
+        if (t == p.E - 1) c.off[t + 1] = end;
+        if (off < 0 || end < off || end > p.rows) set_error(p.err, MOE_DEVERR_BOUNDS);
+        else cnt = (end - off + chunk - 1) / chunk;
     }
-    const int c = (cnt + chunk - 1) / chunk;
-    int s = c;
+    int s = cnt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
         if (lane >= o) s += v;
     }
-    if (warp < 8 && lane == 31) sm[warp] = s;
-    if (t == 0) sm[8] = -1;
+    if (lane == 31) c.warp_sum[warp] = s;
     __syncthreads();
-    if (warp < 8) {
-        for (int w = 0; w < warp; ++w) s += sm[w];
-        const int first = s - c;
-        if (u >= first && u < s) {
-            const int m = u - first;
-            sm[8] = t;
-            sm[9] = off + m * chunk;
-            sm[10] = min(chunk, cnt - m * chunk);
-        }
+    for (int w = 0; w < warp; ++w) s += c.warp_sum[w];
+    if (t < p.E) c.base[t + 1] = s;
+    if (t == 0) c.base[0] = 0;
+}
+// The expert of chunk u < base[E].
+MOE_DEV int expert_of(const Chunks& c, int u, int E) {
+    int lo = 0, hi = E;  // base[lo] <= u < base[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c.base[mid] <= u) lo = mid;
+        else hi = mid;
     }
-    __syncthreads();
-    e = sm[8];
-    row0 = sm[9];
-    n = sm[10];
-    return e >= 0;
+    return lo;
 }
 
 // One output value.

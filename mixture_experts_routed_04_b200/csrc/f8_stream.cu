@@ -8,7 +8,11 @@
 // 4 bytes of K at tig*4 and at 16 + tig*4, but a sum over K may take K in any order,
 // so lane tig holds bytes 16 tig.. of a 64-byte piece and feeds them to two products,
 // with the same bytes of the 8 rows as the B operand. Nothing passes through shared
-// memory. A block of 128 is summed from zero, multiplied by its two scales and added
+// memory, and a block is small (8 warps of 64 to 85 registers), so that three or four
+// of them share an SM and one's start and joint hide behind the others' loads (8 experts'
+// gate and up of 1536 x 4096, 16-bit results: 26.1 us with two blocks of 128
+// registers, 23.4 with three; down of 4096 x 1536 22.5 with three, 17.7 with four; one
+// persistent block with copies ahead through shared memory 40 us). A block of 128 is summed from zero, multiplied by its two scales and added
 // in fp32; the 8 warps' sums are added in order at the end (no atomics).
 // Gated with e4m3 results needs the largest of 128 columns: the 8 blocks that hold
 // them are one cluster and exchange their maxima through its shared memory.
@@ -39,8 +43,57 @@ MOE_DEV uint4 ld_weights(const uint8_t* p, bool in) {
     return in ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
 }
 
+// Blocks of `chunk` rows of the experts, in the experts' order: block `u` is rows
+// [row0, row0 + n) of expert e; false past the last one. Every thread of a block of
+// at least 256 threads calls it (E <= 256: one expert a thread, one pass of scans;
+// a search by row would be a chain of dependent loads). sm: 12 ints.
+MOE_DEV bool find_rows(const Args& p, int u, int chunk, int* sm, int& e, int64_t& row0, int& n) {
+    if (!p.offsets) {
+        e = 0;
+        row0 = int64_t(u) * chunk;
+        n = int(min(int64_t(chunk), p.rows - row0));
+        return n > 0;
+    }
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int off = 0, cnt = 0;
+    if (t < p.E) {
+        off = __ldg(p.offsets + t);
+        cnt = __ldg(p.offsets + t + 1) - off;
+        // offsets outside the buffers (never from moe_permute) are not followed
+        if (off < 0 || cnt < 0 || int64_t(off) + cnt > p.rows) {
+            set_error(p.err, MOE_DEVERR_BOUNDS);
+            cnt = 0;
+        }
+    }
+    const int c = (cnt + chunk - 1) / chunk;
+    int s = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
+        if (lane >= o) s += v;
+    }
+    if (warp < 8 && lane == 31) sm[warp] = s;
+    if (t == 0) sm[8] = -1;
+    __syncthreads();
+    if (warp < 8) {
+        for (int w = 0; w < warp; ++w) s += sm[w];
+        const int first = s - c;
+        if (u >= first && u < s) {
+            const int m = u - first;
+            sm[8] = t;
+            sm[9] = off + m * chunk;
+            sm[10] = min(chunk, cnt - m * chunk);
+        }
+    }
+    __syncthreads();
+    e = sm[8];
+    row0 = sm[9];
+    n = sm[10];
+    return e >= 0;
+}
+
 template <bool GATED, bool E4M3>
-__global__ void __launch_bounds__(kThreads) f8_stream_kernel(const Args p) {
+__global__ void __launch_bounds__(kThreads, GATED ? 3 : 4) f8_stream_kernel(const Args p) {
     constexpr int M = GATED ? 2 : 1;
     __shared__ int found[12];
     __shared__ float part[kWarps][M][kRows][kCols + 1];
@@ -65,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) f8_stream_kernel(const Args p) {
         const uint8_t* arow = p.a + (row0 + gid) * p.K + tig * 16;
         const int r0 = min(2 * tig, nr - 1), r1 = min(2 * tig + 1, nr - 1);  // columns of the product past nr are not kept
         const int sb0 = (e * p.NB + n0 / 128) * p.KB;
-#pragma unroll 2
+#pragma unroll 1
         for (int kb = warp; kb < p.KB; kb += kWarps) {
             const int k = kb * 128;
             const bool ka = k + tig * 16 < p.K, kc = k + 64 + tig * 16 < p.K;
@@ -143,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) f8_stream_kernel(const Args p) {
             cluster_sync_all();  // no block leaves while another reads its maxima
             if (keep) {
                 const float sc = f8_scale(m);
-                const F8Div div(sc);
+                const F8Div div(f8_divisor(m, sc));
                 static_cast<uint8_t*>(p.out)[(row0 + r) * p.N + n0 + c] =
                     uint8_t(pack_e4m3x2(div.fast ? div(v) : __fdiv_rn(v, sc), 0.f) & 0xFFu);
                 if (n0 % 128 == 0 && c == 0) p.h_scale[int64_t(n0 / 128) * p.rows + row0 + r] = sc;

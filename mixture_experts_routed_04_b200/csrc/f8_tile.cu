@@ -27,7 +27,6 @@
 #include <atomic>
 
 #include "f8.cuh"
-#include "tmap.h"
 
 namespace moe {
 
@@ -66,22 +65,19 @@ MOE_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n
 template <int N>
 MOE_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-MOE_DEV void ld16(uint32_t taddr, uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(taddr)
-        : "memory");
-}
-MOE_DEV void wait16(uint32_t (&v)[16]) {
+// Waits for the loads from TMEM, tied to the registers that one of them fills: no use of them moves
+// before the wait.
+MOE_DEV void tmem_ld_wait_for(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
-                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
                  :
                  : "memory");
 }
+
 struct Misc {
     uint64_t full[STAGES], empty[STAGES];
     uint64_t tfull[2], tempty[2];
@@ -91,9 +87,7 @@ struct Misc {
     uint64_t drain;
     uint32_t tmem;
     int abort;
-    int found[12];
-    int base[kMaxE + 1];          // exclusive prefix of the experts' M-tiles
-    int off[kMaxE + 1];           // their row offsets
+    Chunks tiles;                 // the experts' M-tiles
     float sa[SLOTS][BM];          // the rows' scales of a block
     float sb[SLOTS][2];           // the weights': of the tile's two 128-column halves, or gate and up
     int64_t urow0[2];             // by unit parity: what the tile's results need
@@ -110,20 +104,14 @@ struct Unit {
 
 MOE_DEV Unit unit_of(int u, int nt, const Args& p, const Misc* ms) {
     Unit U;
-    const int* base = ms->base;
-    const int g = u / nt;  // as if every M-tile had its n-tiles next to each other: the expert is the same
-    int lo = 0, hi = p.E;  // base[lo] <= g < base[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (base[mid] <= g) lo = mid;
-        else hi = mid;
-    }
+    const int* base = ms->tiles.base;
+    const int lo = expert_of(ms->tiles, u / nt, p.E);  // as if every M-tile had its n-tiles next to each other
     U.e = lo;
     const int mt = base[lo + 1] - base[lo], local = u - base[lo] * nt;
     U.n = local / mt;
     const int m = local - U.n * mt;
-    U.row0 = ms->off[lo] + int64_t(m) * BM;
-    U.rows = int(min(int64_t(BM), ms->off[lo + 1] - U.row0));
+    U.row0 = ms->tiles.off[lo] + int64_t(m) * BM;
+    U.rows = int(min(int64_t(BM), ms->tiles.off[lo + 1] - U.row0));
     return U;
 }
 
@@ -208,42 +196,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     griddep_wait();
     griddep_launch();
-    // the experts' M-tiles, one expert a thread
-    {
-        const int t = threadIdx.x;
-        int cnt = 0;
-        if (!p.offsets) {
-            if (t == 0) {
-                cnt = int((p.rows + BM - 1) / BM);
-                ms->off[0] = 0;
-                ms->off[1] = int(p.rows);
-            }
-        } else if (t < p.E) {
-            const int off = __ldg(p.offsets + t), end = __ldg(p.offsets + t + 1);
-            ms->off[t] = off;
-            if (t == p.E - 1) ms->off[t + 1] = end;
-            if (off < 0 || end < off || end > p.rows) set_error(p.err, MOE_DEVERR_BOUNDS);  // not followed
-            else cnt = (end - off + BM - 1) / BM;
-        }
-        int s = cnt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
-            if (lane >= o) s += v;
-        }
-        if (lane == 31) ms->found[warp] = s;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) s += ms->found[w];
-        if (t < p.E) ms->base[t + 1] = s;
-        if (t == 0) ms->base[0] = 0;
-    }
+    count_chunks(p, BM, ms->tiles);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem_base = ms->tmem;
     const int cols = GATED ? 128 : BN;  // columns of the result a tile
     const int nt = (p.N + cols - 1) / cols;
-    const int total = ms->base[p.E] * nt;
+    const int total = ms->tiles.base[p.E] * nt;
 
     if (warp < FIRST) {
         reg_dec<40>();
@@ -262,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     uint8_t* sa = smem + stage * STAGE;
                     mbar_arrive_expect_tx(ms->full + stage, STAGE);
-                    tma_load_2d(sa, &tmA, ms->full + stage, kb * BK, int(U.row0));
+                    tma_load_3d(sa, &tmA, ms->full + stage, kb * BK, int(U.row0), 0);
                     if (GATED) {
                         tma_load_3d(sa + A_BYTES, &tmB0, ms->full + stage, kb * BK, U.n * 128, U.e);
                         tma_load_3d(sa + A_BYTES + B_BYTES / 2, &tmB1, ms->full + stage, kb * BK, U.n * 128, U.e);
@@ -409,8 +369,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t ch = tb + (h ? c1 : c0);
                     tmem_ld_32x32b_x32(ch, t[0]);
                     tmem_ld_32x32b_x32(ch + 32, t[1]);
-                    tmem_ld_wait(t[0]);
-                    tmem_ld_wait(t[1]);
+                    tmem_ld_wait_for(t[0]);
+                    tmem_ld_wait_for(t[1]);
                     if (h == 1) {
                         tc_fence_before();
                         __syncwarp();
@@ -453,7 +413,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int i = 0; i < NV; ++i) v[i] *= w;
             }
             constexpr int es = OUT == MOE_DT_F32 ? 4 : OUT == MOE_DT_E4M3 ? 1 : 2;
-            float sc = 1.f;
+            float divisor = 1.f;
             if constexpr (OUT == MOE_DT_E4M3) {
                 uint32_t m = 0;  // columns past N are zeros of zero weights
 #pragma unroll
@@ -468,10 +428,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 xph ^= 1u;
 #pragma unroll
                 for (int i = 0; i < PARTS; ++i) m = max(m, ms->amax[par][i][rt]);
-                sc = f8_scale(m);
+                const float sc = f8_scale(m);
                 if (part == 0 && live) p.h_scale[int64_t(un) * p.rows + row] = sc;
+                if (live) divisor = f8_divisor(m, sc);  // rows past the expert's may hold anything
             }
-            const F8Div div(sc);
+            const F8Div div(divisor);
             if constexpr (OUT == MOE_DT_F16) {
                 if (live) {
 #pragma unroll
@@ -537,12 +498,31 @@ cudaError_t go(const CUtensorMap& A, const CUtensorMap& B0, const CUtensorMap& B
                       dim3(THREADS), SMEM, s, A, B0, B1, p);
 }
 
-// Bytes, innermost dimension K; box 128 (K) x `box_rows`, 128-byte swizzle.
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                            cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<EncodeTiledFn>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// Bytes [n, rows, K]; box 128 (K) x `box_rows` x 1, 128-byte swizzle.
 bool map_bytes(CUtensorMap* m, const void* base, int K, int64_t rows, int n, int box_rows) {
-    const uint64_t dims[3] = {uint64_t(K), uint64_t(rows), uint64_t(n)};
-    const uint64_t str[2] = {uint64_t(K), uint64_t(K) * uint64_t(rows)};
-    const uint32_t box[3] = {128, uint32_t(box_rows), 1};
-    return tc::make_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, n ? 3 : 2, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    const EncodeTiledFn enc = encode_fn();
+    const cuuint64_t dims[3] = {cuuint64_t(K), cuuint64_t(rows), cuuint64_t(n)};
+    const cuuint64_t str[2] = {cuuint64_t(K), cuuint64_t(K) * cuuint64_t(rows)};
+    const cuuint32_t box[3] = {BK, cuuint32_t(box_rows), 1}, step[3] = {1, 1, 1};
+    return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, str, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -550,7 +530,7 @@ bool map_bytes(CUtensorMap* m, const void* base, int K, int64_t rows, int n, int
 cudaError_t launch_tile(const Args& p, bool gated, cudaStream_t s) {
     CUtensorMap A, B0, B1;
     const int box = gated ? 128 : BN;
-    if (!map_bytes(&A, p.a, p.K, p.rows, 0, BM) || !map_bytes(&B0, p.b[0], p.K, p.N, p.E, box) ||
+    if (!map_bytes(&A, p.a, p.K, p.rows, 1, BM) || !map_bytes(&B0, p.b[0], p.K, p.N, p.E, box) ||
         !map_bytes(&B1, p.b[1], p.K, p.N, p.E, box))
         return cudaErrorInvalidValue;
     switch (p.out_dt) {

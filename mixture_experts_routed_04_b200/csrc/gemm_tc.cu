@@ -41,7 +41,6 @@
 // raises MOE_DEVERR_TIMEOUT, the CTA drains its copies and MMAs, frees TMEM and
 // returns. Every TMA copy fills only the issuing CTA's shared memory.
 #include "gemm_tc.cuh"
-#include "tmap.h"
 
 namespace moe {
 
@@ -535,8 +534,9 @@ static EncodeTiledFn get_encode() {
     return fn;
 }
 
-bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
-              const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz) {
+// dims/strides innermost first (strides in bytes, rank-1 of them).
+static bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides_bytes, const uint32_t* box, CUtensorMapSwizzle swz) {
     EncodeTiledFn enc = get_encode();
     if (!enc) return false;
     if (rank < 1 || rank > 5) return false;

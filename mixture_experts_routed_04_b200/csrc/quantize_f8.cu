@@ -70,13 +70,13 @@ MOE_DEV void round_chunk(const char* p, int dc, uint8_t* q, float* scales, int l
         quad(k, v);
         m[k] = __reduce_max_sync(0xFFFFFFFFu, amax4_bits(v));
     }
-    float scale, recip;
-    const bool fast = warp_scales(m, scale, recip);
+    float scale, divisor, recip;
+    const bool fast = warp_scales(m, scale, divisor, recip);
     if (lane < kQuads) scales[lane] = scale;
     if (fast) {
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
-            const float s = __shfl_sync(0xFFFFFFFFu, scale, k), nrs = __shfl_sync(0xFFFFFFFFu, -recip, k);
+            const float s = __shfl_sync(0xFFFFFFFFu, divisor, k), nrs = __shfl_sync(0xFFFFFFFFu, -recip, k);
             const int c = (k * 32 + lane) * 4;
             float v[4];
             quad(k, v);
@@ -86,7 +86,7 @@ MOE_DEV void round_chunk(const char* p, int dc, uint8_t* q, float* scales, int l
 #pragma unroll
         for (int k = 0; k < kQuads; ++k) {
             F8Div div;
-            div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
+            div.s = __shfl_sync(0xFFFFFFFFu, divisor, k);
             div.fast = false;
             const int c = (k * 32 + lane) * 4;
             float v[4];
@@ -229,8 +229,9 @@ __global__ void __launch_bounds__(256, F32 ? 2 : 4) quantize_weights_kernel(cons
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, wmax[i]);
-    const F8Div div(f8_scale(m));
-    if (threadIdx.x == 0) s[(int64_t(e) * gridDim.y + nb) * gridDim.x + kb] = div.s;
+    const float scale = f8_scale(m);
+    const F8Div div(f8_divisor(m, scale));
+    if (threadIdx.x == 0) s[(int64_t(e) * gridDim.y + nb) * gridDim.x + kb] = scale;
     if (!TURN) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

@@ -304,19 +304,24 @@ MOE_DEV uint32_t pack4_e4m3(const float* v, const F8Div& div) {
                           pack_e4m3x2(__fdiv_rn(v[2], div.s), __fdiv_rn(v[3], div.s)) << 16;
 }
 
+// What a group whose largest magnitude is m divides by: its scale, or 1 for a group of zeros, whose
+// scale of 2^-126 would take the long way to the same zeros.
+MOE_DEV float f8_divisor(uint32_t m, float scale) { return m ? scale : 1.0f; }
+
 // The scales of a warp's N <= 32 groups of 128 columns from their largest magnitudes m[k], which the
 // warp agrees on: lane k divides for group k, so that the two divisions are done once a warp and not
 // once a lane and group. Warp-uniform result: whether every group's quotients may take the short way.
 template <int N>
-MOE_DEV bool warp_scales(const uint32_t (&m)[N], float& scale, float& recip) {
+MOE_DEV bool warp_scales(const uint32_t (&m)[N], float& scale, float& divisor, float& recip) {
     uint32_t mine = 0;
 #pragma unroll
     for (int k = 0; k < N; ++k)
         if ((threadIdx.x & 31) == k) mine = m[k];
-    const F8Div div(f8_scale(mine));
-    scale = div.s;
+    scale = f8_scale(mine);
+    const F8Div div(f8_divisor(mine, scale));
+    divisor = div.s;
     recip = div.rs;
-    return __all_sync(0xFFFFFFFFu, div.fast || (threadIdx.x & 31) >= N);
+    return __all_sync(0xFFFFFFFFu, div.fast);
 }
 
 // A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes;
@@ -329,12 +334,12 @@ MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64
         const float* x = v[k >> 1] + 4 * (k & 1);
         m[k] = __reduce_max_sync(0xFFFFFFFFu, amax4_bits(x));
     }
-    float scale, recip;
-    const bool fast = warp_scales(m, scale, recip);
+    float scale, divisor, recip;
+    const bool fast = warp_scales(m, scale, divisor, recip);
 #pragma unroll
     for (int k = 0; k < 2 * NV; ++k) {
         F8Div div;
-        div.s = __shfl_sync(0xFFFFFFFFu, scale, k);
+        div.s = __shfl_sync(0xFFFFFFFFu, divisor, k);
         div.rs = __shfl_sync(0xFFFFFFFFu, recip, k);
         div.fast = fast;
         const int c = (k * th + t) * 4;
