@@ -2,22 +2,29 @@
 // expert x 256 weight rows a tile (gated: 128 of gate and 128 of up), persistent,
 // one CTA an SM.
 //
-//   warp 0     TMA producer: per block of 128 along K, the 128 x 128 bytes of the
-//              rows and the 256 x 128 bytes of the weights (128-byte swizzle; past
-//              K and N zeros come in), 4 stages of 48 KB.
-//   warp 1     TMEM and the MMAs: tcgen05.mma kind::f8f6f4, M=128 N=256 K=32, four
-//              a block. Every block of 128 is summed from zero into one of two
-//              256-column accumulators, because its scales are its own.
-//   warps 2-9  the sums: each block's accumulator leaves TMEM as soon as it is done,
-//              is multiplied by its two scales and added in fp32 registers (128
-//              columns of one row a thread), while the MMAs fill the other one. The
-//              scaled sum takes about as many issue slots (128 packed fp32 FMAs and 4
-//              loads of 32 columns a warp and block) as half the MMAs' time (512 cycles
-//              a block), so the tensor pipe stays the longer one.
-//              After the last block: the gate weight or the clamped SwiGLU, the
-//              rounding, and the store, turned through 2 KB of shared memory a warp so
-//              that a store writes 64-byte pieces of 8 rows (32 rows of 16 bytes each
-//              would take 32 passes of the load/store unit).
+//   c[r, n] = sum over blocks b of 128 along K of  sa[b, r] sb[n / 128, b] sum_{k in b} a[r, k] w[n, k]
+//
+//   warp 0      TMA producer: per block along K, the 128 x 128 bytes of the rows and
+//               the 256 x 128 bytes of the weights (128-byte swizzle; past K and N
+//               zeros come in), 4 stages of 48 KB.
+//   warp 1      TMEM and the MMAs: tcgen05.mma kind::f8f6f4, M=128 N=256 K=32, four a
+//               block. Every block of 128 is summed from zero into one of two
+//               256-column accumulators, because its scales are its own.
+//   warp 2      the blocks' scales, 8 blocks ahead, and what a tile's results need.
+//   warps 4-11  the sums: a block's accumulator is read from TMEM as soon as it is
+//               done, 64 columns a load, multiplied by its two scales and added in fp32
+//               registers (128 columns of a row a thread), while the MMAs fill the other
+//               one. After the last block: the gate weight or the clamped SwiGLU, the
+//               rounding, and stores of 32 bytes a lane.
+//
+// What bounds it. Every block brings 48 KB into shared memory and the MMAs read as much: 768 cycles
+// at 128 bytes a cycle, against 512 of the MMAs, so that the feed and the MMAs alone, no sums, take
+// 56 us for 4096 x 4096 x 4096. The rest is the accumulators' way round (MMA, load, sum, hand back),
+// which two of them do not quite hide: 85 us with bf16 results, 1.62 PFLOP/s. 32768 rows of 128 experts:
+// 768 -> 2048 (fp16) 122 us; gate and up 2048 -> 2 x 768, e4m3 results 172 us (1.2 PFLOP/s).
+// Slower when tried: four accumulators of 128 columns (99 against 85: the rows' bytes are read twice),
+// 16 warps of sums, pairs of SMs on 256-row tiles (89 for the dense product, 195 against 122 and 350
+// against 172 for the experts: half the traffic, but every block's accumulator waits for two SMs).
 //
 // Gated with e4m3 results: a row's 128 columns lie in two threads (two warps of a
 // lane quadrant), which exchange their maxima over a barrier of those two warps.
@@ -204,130 +211,133 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int cols = GATED ? 128 : BN;  // columns of the result a tile
     const int nt = (p.N + cols - 1) / cols;
     const int total = ms->tiles.base[p.E] * nt;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait_bounded(bar, parity, &ms->abort, p.err, p.wait_ns);
+    };
 
     if (warp < FIRST) {
         reg_dec<40>();
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer (one thread)
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, issued = 0, issued_par = 0;
+        if (warp == 0) {
+            // ------------------------------------------------ TMA producer (one thread)
+            if (lane == 0) {
+                int stage = 0;
+                uint32_t phase = 0, issued = 0, issued_par = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+                    const Unit U = unit_of(u, nt, p, ms);
+                    for (int kb = 0; kb < p.KB; ++kb) {
+                        if (!wait(ms->empty + stage, phase ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* sa = smem + stage * STAGE;
+                        mbar_arrive_expect_tx(ms->full + stage, STAGE);
+                        tma_load_3d(sa, &tmA, ms->full + stage, kb * BK, int(U.row0), 0);
+                        if (GATED) {
+                            tma_load_3d(sa + A_BYTES, &tmB0, ms->full + stage, kb * BK, U.n * 128, U.e);
+                            tma_load_3d(sa + A_BYTES + B_BYTES / 2, &tmB1, ms->full + stage, kb * BK, U.n * 128, U.e);
+                        } else {
+                            tma_load_3d(sa + A_BYTES, &tmB0, ms->full + stage, kb * BK, U.n * BN, U.e);
+                        }
+                        issued |= 1u << stage;
+                        issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                // on abort, every copy already issued lands before the CTA can exit
+                if (!ok)
+                    for (int s = 0; s < STAGES; ++s)
+                        if (issued >> s & 1u)
+                            mbar_wait_bounded(ms->full + s, (issued_par >> s) & 1u, nullptr, p.err, kDrainLimitNs);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // ------------------------------------------------ MMA issuer (one thread)
+            if (lane == 0) {
+                const uint64_t da = sdesc_sw128(smem_u32(smem), 16, 1024), db = sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
+                int stage = 0, acc = 0;
+                uint32_t phase = 0, acc_phase = 0;
+                bool ok = true;
+                for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
+                    for (int kb = 0; kb < p.KB; ++kb) {
+                        if (!wait(ms->full + stage, phase) || !wait(ms->tempty + acc, acc_phase ^ 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        // addresses in the descriptors are in units of 16 bytes, below 2^14
+                        const uint64_t so = uint64_t(stage * (STAGE / 16));
+#pragma unroll
+                        for (int j = 0; j < BK / 32; ++j)  // 32 bytes of K inside the swizzled rows
+                            umma_f8(tmem_base + uint32_t(acc * BN), da + so + j * 2, db + so + j * 2, j != 0);
+                        umma_commit(ms->tfull + acc);
+                        umma_commit(ms->empty + stage);
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                        acc ^= 1;
+                        if (acc == 0) acc_phase ^= 1u;
+                    }
+                }
+                // every MMA this thread issued has completed before TMEM is freed
+                umma_commit(&ms->drain);
+                mbar_wait_bounded(&ms->drain, 0, nullptr, p.err, kDrainLimitNs);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------------------------ scales
+            // A block's 128 row scales and 2 weight scales: loaded by the warps that use them, a block
+            // ahead, their latency under load was longer than a block.
+            int slot = 0, par = 0;
+            uint32_t phase = 0, uphase = 0;
             bool ok = true;
             for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
                 const Unit U = unit_of(u, nt, p, ms);
-                for (int kb = 0; kb < p.KB; ++kb) {
-                    if (!mbar_wait_bounded(ms->empty + stage, phase ^ 1u, &ms->abort, p.err, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* sa = smem + stage * STAGE;
-                    mbar_arrive_expect_tx(ms->full + stage, STAGE);
-                    tma_load_3d(sa, &tmA, ms->full + stage, kb * BK, int(U.row0), 0);
-                    if (GATED) {
-                        tma_load_3d(sa + A_BYTES, &tmB0, ms->full + stage, kb * BK, U.n * 128, U.e);
-                        tma_load_3d(sa + A_BYTES + B_BYTES / 2, &tmB1, ms->full + stage, kb * BK, U.n * 128, U.e);
-                    } else {
-                        tma_load_3d(sa + A_BYTES, &tmB0, ms->full + stage, kb * BK, U.n * BN, U.e);
-                    }
-                    issued |= 1u << stage;
-                    issued_par = (issued_par & ~(1u << stage)) | (phase << stage);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            // on abort, every copy already issued lands before the CTA can exit
-            if (!ok)
-                for (int s = 0; s < STAGES; ++s)
-                    if (issued >> s & 1u) mbar_wait_bounded(ms->full + s, (issued_par >> s) & 1u, nullptr, p.err, kDrainLimitNs);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer (one thread)
-        if (lane == 0) {
-            const uint64_t da = sdesc_sw128(smem_u32(smem), 16, 1024), db = sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
-            int stage = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-                for (int kb = 0; kb < p.KB; ++kb) {
-                    if (!mbar_wait_bounded(ms->full + stage, phase, &ms->abort, p.err, p.wait_ns) || !mbar_wait_bounded(ms->tempty + acc, acc_phase ^ 1u, &ms->abort, p.err, p.wait_ns)) {
-
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    // addresses in the descriptors are in units of 16 bytes, below 2^14
-                    const uint64_t so = uint64_t(stage * (STAGE / 16));
+                const float* as[4];
 #pragma unroll
-                    for (int j = 0; j < BK / 32; ++j)  // 32 bytes of K inside the swizzled rows
-                        umma_f8(tmem_base + uint32_t(acc * BN), da + so + j * 2, db + so + j * 2, j != 0);
-                    umma_commit(ms->tfull + acc);
-                    umma_commit(ms->empty + stage);
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                    acc ^= 1;
-                    if (acc == 0) acc_phase ^= 1u;
-                }
-            }
-            // every MMA this thread issued has completed before TMEM is freed
-            umma_commit(&ms->drain);
-            mbar_wait_bounded(&ms->drain, 0, nullptr, p.err, kDrainLimitNs);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------ scales
-        // A block's 128 row scales and 2 weight scales, 8 blocks ahead: loaded by the warps
-        // that use them, a block ahead, their latency under load was longer than a block.
-        int slot = 0, par = 0;
-        uint32_t phase = 0, uphase = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
-            const Unit U = unit_of(u, nt, p, ms);
-            const float* as[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) as[i] = p.a_scale + U.row0 + min(i * 32 + lane, U.rows - 1);
-            if (!warp_wait(ms->uempty + par, uphase ^ 1u, ms, p)) {
-                ok = false;
-                break;
-            }
-            if (lane == 0) {
-                ms->urow0[par] = U.row0;
-                ms->urows[par] = U.rows;
-                ms->un[par] = U.n;
-            }
-            if (p.sorted_pair) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ms->uw[par][i * 32 + lane] = row_weight(p, U.row0 + min(i * 32 + lane, U.rows - 1));
-            }
-            mbar_arrive(ms->ufull + par);
-            par ^= 1;
-            if (par == 0) uphase ^= 1u;
-            const int nb = GATED ? U.n : min(U.n * 2 + (lane & 1), p.NB - 1);
-            const float* bs = p.b_scale[GATED ? lane & 1 : 0] + (int64_t(U.e) * p.NB + nb) * p.KB;
-            for (int kb = 0; kb < p.KB; ++kb) {
-                if (!warp_wait(ms->sempty + slot, phase ^ 1u, ms, p)) {
+                for (int i = 0; i < 4; ++i) as[i] = p.a_scale + U.row0 + min(i * 32 + lane, U.rows - 1);
+                if (!warp_wait(ms->uempty + par, uphase ^ 1u, ms, p)) {
                     ok = false;
                     break;
                 }
+                if (lane == 0) {
+                    ms->urow0[par] = U.row0;
+                    ms->urows[par] = U.rows;
+                    ms->un[par] = U.n;
+                }
+                if (p.sorted_pair) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    cp_async_4(smem_u32(&ms->sa[slot][i * 32 + lane]), as[i] + int64_t(kb) * p.rows);
-                if (lane < 2) cp_async_4(smem_u32(&ms->sb[slot][lane]), bs + kb);
-                cp_async_arrive(ms->sfull + slot);
-                if (++slot == SLOTS) {
-                    slot = 0;
-                    phase ^= 1u;
+                    for (int i = 0; i < 4; ++i)
+                        ms->uw[par][i * 32 + lane] = row_weight(p, U.row0 + min(i * 32 + lane, U.rows - 1));
+                }
+                mbar_arrive(ms->ufull + par);
+                par ^= 1;
+                if (par == 0) uphase ^= 1u;
+                const int nb = GATED ? U.n : min(U.n * 2 + (lane & 1), p.NB - 1);
+                const float* bs = p.b_scale[GATED ? lane & 1 : 0] + (int64_t(U.e) * p.NB + nb) * p.KB;
+                for (int kb = 0; kb < p.KB; ++kb) {
+                    if (!warp_wait(ms->sempty + slot, phase ^ 1u, ms, p)) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        cp_async_4(smem_u32(&ms->sa[slot][i * 32 + lane]), as[i] + int64_t(kb) * p.rows);
+                    if (lane < 2) cp_async_4(smem_u32(&ms->sb[slot][lane]), bs + kb);
+                    cp_async_arrive(ms->sfull + slot);
+                    if (++slot == SLOTS) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
+            cp_async_wait_all();
+            __syncwarp();
         }
-        cp_async_wait_all();
-        __syncwarp();
-    }
     } else {
         reg_inc<232>();
         // ------------------------------------------------ scaled sums and results

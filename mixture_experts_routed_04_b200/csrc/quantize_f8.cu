@@ -2,11 +2,15 @@
 // moe_quantize_f8 (rows, gathered by token for the experts' products) and
 // moe_quantize_f8_weights (once, at load time).
 //
-// Rows: a warp takes up to 1024 columns of a row, a block of 128 at 4 columns a lane, with
-// all of its loads in flight first; one warp maximum finds a block's largest magnitude
-// (rows.cuh). Bytes: 2 to 4 a value in, 1 out; a gathered
-// row is read k times, from L2 for a prompt's x. Weights: a block of threads takes
-// one 128 x 128 block into registers; given [K, N] it turns it in shared memory.
+// Rows: a warp takes up to 1024 columns of a row in 16-byte pieces, with all of its
+// loads in flight first. The largest magnitudes of the 8 blocks of 128 in them are found
+// together: halves of the lanes swap the partial maxima of half of the blocks, so that 5 exchanges
+// (9 for fp32) do for all, and at the end every four lanes hold one block's and divide for it.
+// 16-bit values are compared two at a time as they were read (bit patterns of magnitudes sort
+// like the magnitudes, NaN above infinity), and widened only to be rounded.
+// Bytes: 2 to 4 a value in, 1 out; a gathered row is read k times, from L2 for a prompt's x.
+// Weights: a block of threads takes one 128 x 128 block into registers; given [K, N] it turns it
+// in shared memory.
 #include <algorithm>
 
 #include "rows.cuh"
@@ -15,83 +19,87 @@ namespace moe {
 
 namespace {
 
-constexpr int kQuads = 8;                // quads a lane: a warp holds 1024 columns at once
-constexpr int kChunk = 32 * 4 * kQuads;
+constexpr int kChunk = 1024;             // columns a warp holds at once
 constexpr int kSpan = 32 * 128;          // columns whose scales a warp gathers, one a lane
 
-// Rounds columns c0 .. c0 + dc (<= kChunk) of a row; scales[k]: of the k-th 128 of them. The values stay
-// as they were read (a third of the registers of fp32 copies of bf16) between the groups' largest
-// magnitudes and their rounding.
-// FULL: dc is kChunk.
+MOE_DEV uint32_t max_u16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Rounds columns c0 .. c0 + dc (<= kChunk) of a row; scales[g]: of the g-th 128 of them.
+// FULL: dc is kChunk. DT: the values' type; PER of them are one piece of 16 bytes, and piece k of the
+// lane holds columns (k * 32 + lane) * PER on. VEC: rows start on 16 bytes.
 template <bool VEC, int DT, bool FULL>
 MOE_DEV void round_chunk(const char* p, int dc, uint8_t* q, float* scales, int lane) {
-    constexpr bool F32 = DT == MOE_DT_F32, bf16 = DT == MOE_DT_BF16;
-    uint4 raw[F32 ? kQuads : kQuads / 2];
-    auto quad = [&](int k, float* v) {
-        if (F32) {
-            const uint4 a = raw[k];
-            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
-            v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-        } else {
-            const uint4 a = raw[k >> 1];
-            unpack4(k & 1 ? make_uint2(a.z, a.w) : make_uint2(a.x, a.y), bf16, v);
-        }
-    };
+    constexpr bool F32 = DT == MOE_DT_F32;
+    constexpr int PER = F32 ? 4 : 8, N = kChunk / (32 * PER);  // pieces a lane
+    uint4 raw[N];
 #pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-        const int c = (k * 32 + lane) * 4;
-        uint4 a = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < N; ++k) {
+        const int c = (k * 32 + lane) * PER;
+        raw[k] = make_uint4(0, 0, 0, 0);
         if (FULL || c < dc) {  // K is a multiple of 16
-            if (F32) {
+            if (VEC) {
+                raw[k] = reinterpret_cast<const uint4*>(p)[k * 32 + lane];
+            } else if (F32) {
                 const uint32_t* x = reinterpret_cast<const uint32_t*>(p) + c;
-                a = VEC ? *reinterpret_cast<const uint4*>(x) : make_uint4(x[0], x[1], x[2], x[3]);
+                raw[k] = make_uint4(x[0], x[1], x[2], x[3]);
             } else {
                 const uint16_t* x = reinterpret_cast<const uint16_t*>(p) + c;
-                const uint2 h = VEC ? *reinterpret_cast<const uint2*>(x)
-                                    : make_uint2(x[0] | uint32_t(x[1]) << 16, x[2] | uint32_t(x[3]) << 16);
-                a.x = h.x;
-                a.y = h.y;
+                raw[k] = make_uint4(x[0] | uint32_t(x[1]) << 16, x[2] | uint32_t(x[3]) << 16,
+                                    x[4] | uint32_t(x[5]) << 16, x[6] | uint32_t(x[7]) << 16);
             }
         }
-        if (F32) {
-            raw[k] = a;
-        } else if (k & 1) {
-            raw[k >> 1].z = a.x;
-            raw[k >> 1].w = a.y;
+    }
+    // magnitudes: fp32 one a word, 16 bits two
+    auto larger = [](uint32_t a, uint32_t b) { return F32 ? max(a, b) : max_u16x2(a, b); };
+    constexpr uint32_t kMagnitude = F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
+    uint32_t m[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        m[k] = larger(larger(raw[k].x & kMagnitude, raw[k].y & kMagnitude),
+                      larger(raw[k].z & kMagnitude, raw[k].w & kMagnitude));
+    // a block of 128 columns: piece k of 32 lanes (fp32) or of 16. Lanes `o` apart keep the maxima of
+    // half of the pieces each, until one is left: that of piece (lane >> 2) % N.
+    int o = F32 ? 16 : 8;
+#pragma unroll
+    for (int h = N / 2; h >= 1; h >>= 1, o >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int i = 0; i < h; ++i) {
+            const uint32_t keep = upper ? m[i + h] : m[i], give = upper ? m[i] : m[i + h];
+            m[i] = larger(keep, __shfl_xor_sync(0xFFFFFFFFu, give, o));
+        }
+    }
+#pragma unroll
+    for (; o >= 1; o >>= 1) m[0] = larger(m[0], __shfl_xor_sync(0xFFFFFFFFu, m[0], o));
+    uint32_t top = m[0];
+    if (!F32) {
+        top = max(top & 0xFFFFu, top >> 16);
+        top = DT == MOE_DT_BF16 ? top << 16 : abs_bits(f16_lo(top));
+    }
+    const float scale = f8_scale(top);
+    const F8Div mine(f8_divisor(top, scale));
+    if ((lane & 3) == 0) scales[F32 ? lane >> 2 : (lane >> 2) % 4 * 2 + (lane >> 4)] = scale;
+    const bool fast = __all_sync(0xFFFFFFFFu, mine.fast);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int from = F32 ? k * 4 : (lane & 16) | k * 4, c = (k * 32 + lane) * PER;
+        F8Div div;
+        div.s = __shfl_sync(0xFFFFFFFFu, mine.s, from);
+        div.rs = __shfl_sync(0xFFFFFFFFu, mine.rs, from);
+        div.fast = fast;  // not with a tiny, infinite or NaN scale among them
+        if (!FULL && c >= dc) continue;
+        if constexpr (F32) {
+            const float v[4] = {__uint_as_float(raw[k].x), __uint_as_float(raw[k].y), __uint_as_float(raw[k].z),
+                                __uint_as_float(raw[k].w)};
+            *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v, div);
         } else {
-            raw[k >> 1].x = a.x;
-            raw[k >> 1].y = a.y;
-        }
-    }
-    uint32_t m[kQuads];
-#pragma unroll
-    for (int k = 0; k < kQuads; ++k) {
-        float v[4];
-        quad(k, v);
-        m[k] = __reduce_max_sync(0xFFFFFFFFu, amax4_bits(v));
-    }
-    float scale, divisor, recip;
-    const bool fast = warp_scales(m, scale, divisor, recip);
-    if (lane < kQuads) scales[lane] = scale;
-    if (fast) {
-#pragma unroll
-        for (int k = 0; k < kQuads; ++k) {
-            const float s = __shfl_sync(0xFFFFFFFFu, divisor, k), nrs = __shfl_sync(0xFFFFFFFFu, -recip, k);
-            const int c = (k * 32 + lane) * 4;
-            float v[4];
-            quad(k, v);
-            if (FULL || c < dc) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3_fast(v, s, nrs);
-        }
-    } else {  // a tiny, infinite or NaN scale among them
-#pragma unroll
-        for (int k = 0; k < kQuads; ++k) {
-            F8Div div;
-            div.s = __shfl_sync(0xFFFFFFFFu, divisor, k);
-            div.fast = false;
-            const int c = (k * 32 + lane) * 4;
-            float v[4];
-            quad(k, v);
-            if (c < dc) *reinterpret_cast<uint32_t*>(q + c) = pack4_e4m3(v, div);
+            float v[8];
+            unpack8(raw[k], DT == MOE_DT_BF16, v);
+            *reinterpret_cast<uint2*>(q + c) = make_uint2(pack4_e4m3(v, div), pack4_e4m3(v + 4, div));
         }
     }
 }
@@ -302,7 +310,7 @@ int moe_quantize_f8(int64_t rows, int32_t K, const void* x, int32_t x_dtype, int
     const size_t es = x_dtype == MOE_DT_F32 ? 4 : 2;
     if (!aligned(q, 16) || !aligned(s, 4) || !aligned(x, es) || !aligned(row_index, 4) || !aligned(n_rows, 4))
         return MOE_ERR_MISALIGNED;
-    const bool vec = aligned(x, 4 * es) && ld % 4 == 0;
+    const bool vec = aligned(x, 16) && ld * int64_t(es) % 16 == 0;
     // 8 rows a warp once that gives every scheduler of every SM four warps
     const bool many = rows >= int64_t(num_sms()) * 16 * 8;
     const int64_t units = many ? (rows + 7) / 8 : rows;

@@ -52,13 +52,6 @@ MOE_DEV uint2 pack4(const float* v, bool bf16) {
     return bf16 ? make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]))
                 : make_uint2(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]));
 }
-MOE_DEV uint4 pack8(const float (&v)[8], bool bf16) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = bf16 ? cvt_bf16x2(v[2 * i], v[2 * i + 1]) : pack_f16x2(v[2 * i], v[2 * i + 1]);
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // A row spread over `th` threads, NV groups of 8 elements each: two quads of 4.
 //   kScalarRow: element j of group v sits at (v*8 + j)*th + t, so that any length, stride and

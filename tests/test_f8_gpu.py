@@ -224,6 +224,13 @@ def test_matmul(shape, variant):
     check_matmul(*shape, "f32", variant, False)
 
 
+# Dense products of more tiles than SMs: several tiles a block, the last ones nearly empty, ragged, full.
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1300, 1040, 4104, 1, 0), (1537, 272, 3592, 1, 0), (5001, 128, 2048, 1, 0)], ids=str)
+def test_matmul_many_tiles(shape, out):
+    check_matmul(*shape, out, "tensor", out == "bf16")
+
+
 @pytest.mark.parametrize("variant", ["tensor", "stream"])
 @pytest.mark.parametrize("out", ["bf16", "f16"])
 @pytest.mark.parametrize("shape", [(5, 272, 200, 1, 0), (333, 272, 1000, 6, 9), (260, 768, 64, 1, 0)], ids=str)
@@ -236,11 +243,21 @@ def test_matmul_weighted_16_bits(shape, out, variant):
 @pytest.mark.parametrize("limit", [0.0, 2.0])
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_gated(shape, limit, out, variant):
-    R, K, N, E, tail = shape
-    if out == "e4m3" and N % 16:
+    if out == "e4m3" and shape[2] % 16:
         pytest.skip("rows in 8 bits are multiples of 16")
     if out == "bf16" and limit:
         pytest.skip("covered by the others")
+    check_gated(shape, limit, out, variant)
+
+
+@pytest.mark.parametrize("out", ["e4m3", "f32", "bf16"])
+@pytest.mark.parametrize("shape", [(1300, 1040, 1872, 1, 0), (2047, 256, 1296, 1, 0)], ids=str)
+def test_gated_many_tiles(shape, out):
+    check_gated(shape, 2.0, out, "tensor")
+
+
+def check_gated(shape, limit, out, variant):
+    R, K, N, E, tail = shape
     rng = np.random.default_rng([R, K, N, E, 5])
     a, sa = rows8(rng, R, K)
     wg, sg = weights8(rng, E, N, K)
