@@ -601,9 +601,9 @@ MOE_API int moe_norm_residual_backward(const moe_norm_params* p, const void* y, 
  *   weights  q [E, N, K] bytes, K-major; scales [E, ceil(N/128), ceil(K/128)]
  *   s = max(amax / 448, 2^-126), q = e4m3(x / s), nearest even; an infinity or a NaN makes its
  *   whole block read back as NaN.
- * K is a multiple of 16 up to MOE_F8_MAX_K, N of 8; the last block of either may be partial. Byte tensors lie on 16
- * bytes (MOE_ERR_MISALIGNED). Rows by expert are as moe_permute leaves them: expert e has rows
- * [offsets[e], offsets[e+1]); rows from offsets[E] on are neither read nor written.
+ * K is a multiple of 16 up to MOE_F8_MAX_K, N of 8 with E * N <= 2^31 - 256; the last block of either may be
+ * partial. Byte tensors lie on 16 bytes (MOE_ERR_MISALIGNED). Rows by expert are as moe_permute leaves them: expert e has rows
+ * [offsets[e], offsets[e+1]); rows from offsets[E] on have no part in any result and are not written.
  */
 
 #define MOE_F8_MAX_K (1 << 20)

@@ -388,6 +388,10 @@ def _fits(what, stream, *specs):
         raise MoeError(f"{what}: {name} is {t.dtype}" if t.dtype not in dtypes else f"{what}: {name} is not contiguous")
 
 
+def _ws_spec(ws):
+    return "ws", ws, () if ws is None else ws.shape, _dtypes("u8"), True
+
+
 _dtype_table = None
 
 
@@ -457,7 +461,7 @@ def norm_backward(p: NormParams, x, dy, mean, rstd, dx, ws=None, weight=None, dr
     _fits("moe_norm_backward", stream, ("x", x, row, st, False), ("dy", dy, row, _dtypes(p.block_dtype), False),
           ("dres", dres, row, st, False), ("dx", dx, row, st, False), ("weight", weight, (p.d,), par, True),
           ("mean", mean, (p.T,), f32, True), ("rstd", rstd, (p.T,), f32, True), ("dw", dw, (p.d,), f32, True),
-          ("db", db, (p.d,), f32, True))
+          ("db", db, (p.d,), f32, True), _ws_spec(ws))
     _rows_ok("moe_norm_backward", p, p.ld_stream, x=x, dres=dres, dx=dx)
     _rows_ok("moe_norm_backward", p, p.ld_block, dy=dy)
     check(lib().moe_norm_backward(ctypes.byref(p), _p(x), _p(weight), _p(dy), _p(dres), _p(mean), _p(rstd), _p(dx),
@@ -496,7 +500,7 @@ def norm_residual_backward(p: NormParams, y, dout, mean, rstd, dy, ws=None, weig
           ("dresid", dresid, row, st, False), ("dy", dy, row, bl, False), ("weight", weight, vec, par, True),
           ("bias", bias, vec, par, True), ("gate", gate, g, par, True), ("mean", mean, tok, f32, True),
           ("rstd", rstd, tok, f32, True), ("dw", dw, vec, f32, True), ("db", db, vec, f32, True),
-          ("dgate", dgate, g, f32, True))
+          ("dgate", dgate, g, f32, True), _ws_spec(ws))
     _rows_ok("moe_norm_residual_backward", p, p.ld_stream, dout=dout, dresid=dresid)
     _rows_ok("moe_norm_residual_backward", p, p.ld_block, y=y, dy=dy)
     check(lib().moe_norm_residual_backward(ctypes.byref(p), _p(y), _p(weight), _p(bias), _p(gate), _p(dout), _p(mean),
@@ -529,8 +533,9 @@ def quantize_f8(x, q, s, ws, row_index=None, n_rows=None, stream=None):
     _fits("moe_quantize_f8", stream, ("x", x, (x.shape[0], K), _dtypes("rows"), False),
           ("q", q, (rows, K), _dtypes(DT_E4M3), True), ("s", s, ((K + 127) // 128, rows), _dtypes(DT_F32), True),
           ("row_index", row_index, (rows,), _dtypes("i32"), True),
-          ("n_rows", n_rows, () if n_rows is None else n_rows.shape, _dtypes("i32"), True),
-          ("ws", ws, ws.shape, _dtypes("u8"), True))
+          ("n_rows", n_rows, () if n_rows is None else n_rows.shape, _dtypes("i32"), True), _ws_spec(ws))
+    if n_rows is not None and n_rows.numel() == 0:
+        raise MoeError("moe_quantize_f8: n_rows is empty")
     if x.shape[0] > 0 and (K > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < K):
         raise MoeError(f"moe_quantize_f8: x has strides {x.stride()}")
     check(lib().moe_quantize_f8(rows, K, _p(x), _dt(x), x.stride(0) if x.shape[0] > 1 else K, x.shape[0],
@@ -550,10 +555,10 @@ def quantize_f8_weights(w, q, s, transposed=False, stream=None):
 
 def _f8_specs(p, a, a_scale, offsets, ws, *weights):
     """What _fits checks of the operands every product takes; weights: (name, tensor, scales)."""
-    f8, f32, i32, u8 = _dtypes(DT_E4M3), _dtypes(DT_F32), _dtypes("i32"), _dtypes("u8")
+    f8, f32, i32 = _dtypes(DT_E4M3), _dtypes(DT_F32), _dtypes("i32")
     kb, nb = (p.K + 127) // 128, (p.N + 127) // 128
     specs = [("a", a, (p.rows, p.K), f8, True), ("a_scale", a_scale, (kb, p.rows), f32, True),
-             ("offsets", offsets, (p.E + 1,), i32, True), ("ws", ws, ws.shape, u8, True)]
+             ("offsets", offsets, (p.E + 1,), i32, True), _ws_spec(ws)]
     for name, t, s in weights:
         specs += [(name, t, (p.E, p.N, p.K), f8, True), ("the scales of " + name, s, (p.E, nb, kb), f32, True)]
     return specs

@@ -16,13 +16,14 @@ bool al(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n -
 
 int check_params(const moe_f8_params* p) {
     if (!p || p->rows < 0 || p->rows >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
-    if (p->K < 16 || p->K % 16 || p->K > MOE_F8_MAX_K || p->N < 8 || p->N % 8 || p->E < 1 || p->E > kMaxE) return MOE_ERR_INVALID_ARG;
+    if (p->K < 16 || p->K % 16 || p->K > MOE_F8_MAX_K || p->N < 8 || p->N % 8 || p->E < 1 || p->E > kMaxE)
+        return MOE_ERR_INVALID_ARG;
     if (p->out_dtype < MOE_DT_F32 || p->out_dtype > MOE_DT_E4M3) return MOE_ERR_INVALID_ARG;
     if (p->variant < MOE_VARIANT_AUTO || p->variant > MOE_VARIANT_STREAM) return MOE_ERR_INVALID_ARG;
     if (!(p->swiglu_limit >= -3.4e38f && p->swiglu_limit <= 3.4e38f)) return MOE_ERR_INVALID_ARG;
-    // weight rows and scale blocks are counted in 32 bits
-    if (int64_t(p->N) * p->E >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
-    if (int64_t((p->N + 127) / 128) * ((p->K + 127) / 128) * p->E >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+    // weight rows, rounded up to tiles of 256, and scale blocks are counted in 32 bits
+    if (int64_t(p->N) * p->E > (int64_t(1) << 31) - 256) return MOE_ERR_INVALID_ARG;
+    if ((int64_t(p->N) + 127) / 128 * ((p->K + 127) / 128) * p->E >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
 }
 

@@ -759,6 +759,7 @@ int moe_norm_forward(const moe_norm_params* p, const void* x, const void* weight
     for (const void* v : {weight, bias})
         if (!rows_vec(v, p->d, p->d, p->param_dtype)) vec = 0;
     if ((st = check_f8_rows(q8, s8, p->d, vec)) != MOE_OK) return st;
+    if (x == y && (p->stream_dtype != p->block_dtype || lds != ldb)) return MOE_ERR_INVALID_ARG;  // rows over others
     NormArgs a{};
     a.x = x; a.weight = weight; a.bias = bias; a.y = y; a.q8 = q8; a.s8 = s8; a.mean = mean; a.rstd = rstd;
     a.ld_stream = lds; a.ld_block = ldb; a.T = p->T; a.d = p->d; a.kind = p->kind;

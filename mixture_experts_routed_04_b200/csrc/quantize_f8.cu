@@ -339,7 +339,7 @@ int moe_quantize_f8_weights(int32_t E, int32_t N, int32_t K, const void* w, int3
     if (E < 1 || E > 65535 || N < 8 || N % 8 || K < 16 || K % 16 || K > MOE_F8_MAX_K || (transposed != 0 && transposed != 1))
         return MOE_ERR_INVALID_ARG;
     if (w_dtype < MOE_DT_F32 || w_dtype > MOE_DT_F16) return MOE_ERR_INVALID_ARG;
-    if ((N + 127) / 128 > 65535 || int64_t(N) * K >= (int64_t(1) << 40)) return MOE_ERR_INVALID_ARG;
+    if ((int64_t(N) + 127) / 128 > 65535 || int64_t(N) * K >= (int64_t(1) << 40)) return MOE_ERR_INVALID_ARG;
     if (!w || !q || !s) return MOE_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(s, 4) || !aligned(w, w_dtype == MOE_DT_F32 ? 4 : 2)) return MOE_ERR_MISALIGNED;
     // rows of [N, K] are 16-byte multiples (K: a multiple of 16), of [K, N] too (N: of 8)

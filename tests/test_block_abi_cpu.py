@@ -40,6 +40,8 @@ def test_norm_buffers(lib):
     assert norm(lib, p, x=None) == INVALID
     assert norm(lib, p, y=None) == INVALID                       # neither y nor q8
     assert norm(lib, p, q8=P) == INVALID                         # q8 without its scales
+    assert norm(lib, b.norm_params(4, 64, block_dtype=b.DT_BF16)) == INVALID  # in place over rows of another type
+    assert norm(lib, b.norm_params(4, 64, block_dtype=b.DT_F32, ld_block=72)) == INVALID  # or of another stride
     assert norm(lib, p, x=ctypes.c_void_p(4098)) == MISALIGNED   # fp32 at an odd half word
     assert norm(lib, p, q8=ctypes.c_void_p(4100), s8=P) == MISALIGNED
     assert norm(lib, b.norm_params(4, 24), q8=P, s8=P) == INVALID
@@ -84,7 +86,7 @@ def test_empty_batches_need_no_buffers(lib):
 
 @pytest.mark.parametrize("over", [dict(rows=-1), dict(rows=1 << 31), dict(K=8), dict(K=24), dict(N=4), dict(N=12), dict(E=0),
                                   dict(E=257), dict(out_dtype=4), dict(variant=3), dict(swiglu_limit=float("nan")),
-                                  dict(N=1 << 24, E=256)])
+                                  dict(N=1 << 24, E=256), dict(N=(1 << 31) - 8)])
 def test_f8_params(lib, over):
     kw = dict(rows=4, K=64, N=64)
     kw.update(over)
@@ -123,4 +125,5 @@ def test_f8_buffers(lib):
     def weights(E=1, N=64, K=64, w=P, dt=b.DT_BF16, t=0, q=P):
         return lib.moe_quantize_f8_weights(E, N, K, w, dt, t, q, P, None)
     assert weights(E=0) == INVALID and weights(N=12) == INVALID and weights(K=24) == INVALID and weights(t=2) == INVALID
+    assert weights(N=(1 << 31) - 8) == INVALID
     assert weights(w=None) == INVALID and weights(q=odd) == MISALIGNED and weights(dt=3) == INVALID

@@ -407,3 +407,46 @@ def test_waits_that_run_out_are_reported():
     assert err in (0, b.DEVERR_TIMEOUT)
     b.clear_error(ws)
     check_matmul(R, K, N, 1, 0, "f32", "tensor", False)
+
+
+def test_buffers_elsewhere_are_refused():
+    x, q, s = torch.zeros(4, 64, device="cuda"), torch.empty(4, 64, dtype=torch.uint8, device="cuda"), torch.empty(1, 4, device="cuda")
+    with pytest.raises(b.MoeError):
+        b.quantize_f8(x, q, s, torch.zeros(256, dtype=torch.uint8))            # the host's memory
+    with pytest.raises(b.MoeError):
+        b.quantize_f8(x, q, s, torch.zeros(256, device="cuda"))                # not bytes
+    with pytest.raises(b.MoeError):
+        b.quantize_f8(x, q, s, ws256(), n_rows=torch.empty(0, dtype=torch.int32, device="cuda"))
+    p = b.norm_params(4, 64)
+    st = torch.empty(4, device="cuda")
+    with pytest.raises(b.MoeError):
+        b.norm_backward(p, x, x.bfloat16(), st, st, torch.empty_like(x), torch.zeros(1 << 20, dtype=torch.uint8),
+                        weight=torch.ones(64, device="cuda"), dw=torch.empty(64, device="cuda"))
+
+
+@pytest.mark.parametrize("out", ["e4m3", "bf16"])
+def test_tiles_with_tiny_wait_limit_report_and_recover(out):
+    rng = np.random.default_rng(11)
+    R, K, N, E = 700, 1040, 528, 5
+    a, sa = rows8(rng, R, K)
+    wg, sg = weights8(rng, E, N, K)
+    wu, su = weights8(rng, E, N, K)
+    off = torch.from_numpy(split(rng, R, E)).cuda()
+    p = b.f8_params(R, K, N, E, out_dtype=b.DT_E4M3 if out == "e4m3" else b.DT_BF16, variant=b.VARIANT_TENSOR)
+    h = torch.empty(R, N, dtype=torch.uint8 if out == "e4m3" else torch.bfloat16, device="cuda")
+    hs = torch.empty((N + 127) // 128, R, device="cuda") if out == "e4m3" else None
+    pm = b.f8_params(R, K, N, E, out_dtype=b.DT_F32, variant=b.VARIANT_TENSOR)
+    c = torch.empty(R, N, device="cuda")
+    ws = b.f8_workspace(p)
+    b.set_wait_limit_ns(1)
+    try:
+        for _ in range(3):
+            b.gated_f8(p, a, sa, wg, sg, wu, su, h, ws, h_scale=hs, offsets=off)
+            b.matmul_f8(pm, a, sa, wg, sg, c, ws, offsets=off)
+        torch.cuda.synchronize()
+    finally:
+        b.set_wait_limit_ns(0)
+    err = b.get_error(ws)
+    assert err & ~b.DEVERR_TIMEOUT == 0, f"unexpected error bits {err:#x}"
+    check_gated((R, K, N, E, 0), 0.0, out, "tensor")
+    check_matmul(R, K, N, E, 0, "f32", "tensor", False)
