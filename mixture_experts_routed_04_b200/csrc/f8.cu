@@ -67,8 +67,8 @@ Args args_of(const moe_f8_params* p, const uint8_t* a, const float* a_scale, con
 // block, each tile's blocks one after the other, however few its rows are. Estimates in us of B200
 // runs (stream / tiles): one dense product of 4096 x 4096, 8 rows 5.2 / 21.6, 32 rows 12.0 / 21.6,
 // 128 rows 39 / 24; 1024 x 1024, 128 rows 5.8 / 10.2; 768 -> 8192, 32 rows 7.7 / 7.4; 8 experts' gate
-// and up of 1536 x 4096, one row each 30.7 / 35.0, 64 experts with two rows each 220 / 145; down of
-// 4096 x 1536, 8 experts 17.8 / 16.4.
+// and up of 1536 x 4096, one row each 26.3 / 34 to 39, 64 experts with two rows each 189 / 150; down of
+// 4096 x 1536, 8 experts 15.5 / 15.4 to 17.7.
 bool takes_stream(const Args& x, bool gated) {
     const double touched = double(std::min<int64_t>(x.rows, x.E));
     const double chunks = x.offsets ? std::max(touched, x.rows / 8.0) : std::ceil(x.rows / 8.0);
