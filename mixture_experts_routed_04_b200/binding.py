@@ -374,11 +374,11 @@ def _fits(what, stream, *specs):
     """Checks tensors given as (name, tensor, shape, dtypes, dense): on the device the call runs on, of
     the shape and one of the dtypes, contiguous where dense is true. None passes."""
     import torch
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()  # as _stream does: a third of torch.cuda.current_device()'s time
     if stream is not None and stream.device_index != dev:
         raise MoeError(f"{what}: the stream is not on the current device")
     for name, t, shape, dtypes, dense in specs:
-        if t is None or (t.shape == shape and t.dtype in dtypes and t.get_device() == dev and
+        if t is None or (t.get_device() == dev and t.dtype in dtypes and t.shape == shape and
                          (not dense or t.is_contiguous())):
             continue
         if t.get_device() != dev:
@@ -430,9 +430,10 @@ def _norm_grads(dw, db, dgate) -> NormGrads:
 
 def _rows_ok(what, p, ld, **tensors):
     """Row tensors: elements next to each other and the params' stride from row to row."""
-    ld = ld or p.d
+    d = p.d
+    ld = ld or d
     for name, t in tensors.items():
-        if t is None or t.is_contiguous() and ld == p.d:
+        if t is None or ld == d and t.is_contiguous():
             continue
         if t.shape[0] > 0 and (t.stride(1) != 1 and t.shape[1] > 1 or t.shape[0] > 1 and t.stride(0) != ld):
             raise MoeError(f"{what}: {name} has strides {t.stride()}, the params say {(ld, 1)}")
