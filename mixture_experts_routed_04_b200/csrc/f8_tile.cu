@@ -19,10 +19,12 @@
 //
 // What bounds it. Every block brings 48 KB into shared memory and the MMAs read as much: 768 cycles
 // at 128 bytes a cycle, against 512 of the MMAs, so that the feed and the MMAs alone, no sums, take
-// 56 us for 4096 x 4096 x 4096. The rest is the accumulators' way round (MMA, load, sum, hand back),
-// which two of them do not quite hide: 85 us with bf16 results, 1.62 PFLOP/s. 32768 rows of 128 experts:
+// 56 us for 4096 x 4096 x 4096. The tiles' ends, where every CTA writes its 64 KB at once, add 12, the
+// accumulators' loads 2 and the sums' FMAs 16, which the accumulators' way round (MMA, load, sum, hand
+// back) does not hide: 85 us with bf16 results, 1.62 PFLOP/s. 32768 rows of 128 experts:
 // 768 -> 2048 (fp16) 122 us; gate and up 2048 -> 2 x 768, e4m3 results 172 us (1.2 PFLOP/s).
-// Slower when tried: four accumulators of 128 columns (99 against 85: the rows' bytes are read twice),
+// No faster when tried: three loads of 32 columns in turn with their sums. Slower: the next block's
+// scales read behind a load (101), four accumulators of 128 columns (99 against 85: the rows' bytes are read twice),
 // 16 warps of sums, pairs of SMs on 256-row tiles (89 for the dense product, 195 against 122 and 350
 // against 172 for the experts: half the traffic, but every block's accumulator waits for two SMs).
 //
