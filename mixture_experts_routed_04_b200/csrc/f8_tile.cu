@@ -24,9 +24,9 @@
 // back) does not hide: 85 us with bf16 results, 1.62 PFLOP/s. 32768 rows of 128 experts:
 // 768 -> 2048 (fp16) 122 us; gate and up 2048 -> 2 x 768, e4m3 results 172 us (1.2 PFLOP/s).
 // No faster when tried: three loads of 32 columns in turn with their sums. Slower: the next block's
-// scales read behind a load (101), four accumulators of 128 columns (99 against 85: the rows' bytes are read twice),
-// 16 warps of sums, pairs of SMs on 256-row tiles (89 for the dense product, 195 against 122 and 350
-// against 172 for the experts: half the traffic, but every block's accumulator waits for two SMs).
+// scales read behind a load (101), four accumulators of 128 columns (99: the rows' bytes are read
+// twice), 16 warps of sums, pairs of SMs on 256-row tiles (89 for this product, the peer's hand-back
+// without a release: half the traffic, but every block's accumulator waits for two SMs).
 //
 // Gated with e4m3 results: a row's 128 columns lie in two threads (two warps of a
 // lane quadrant), which exchange their maxima over a barrier of those two warps.
