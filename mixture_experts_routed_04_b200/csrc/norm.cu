@@ -251,7 +251,8 @@ __global__ void __launch_bounds__(kThreads, POST ? 2 : 3) norm_forward_kernel(co
         }
         if (a.y && live) store_row<NV, L>(v, at_row(a.y, r, a.ld_block, a.block_dt), d, a.block_dt, th, t);
         if constexpr (L != kScalarRow) {
-            if (a.q8) store_row_e4m3<NV, L == kScalarRow ? kVecRow : L>(v, a.q8 + (live ? r : 0) * d, a.s8 + (live ? r : 0), a.T, dl, th, t);
+            // `live` is one value a warp; a full row's stores have no bound of their own that could keep a row past T back
+            if (a.q8 && live) store_row_e4m3<NV, L>(v, a.q8 + r * d, a.s8 + r, a.T, d, th, t);
         }
         if constexpr (STAGED) {  // the row is in registers: its place takes the row `depth` on
             __syncwarp();

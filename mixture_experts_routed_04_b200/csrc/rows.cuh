@@ -318,7 +318,8 @@ MOE_DEV bool warp_scales(const uint32_t (&m)[N], float& scale, float& divisor, f
 }
 
 // A row in a vector layout to e4m3: a warp's quads are a group of 128 columns. q: the row's bytes;
-// s: scale of column group 0, the next ones `lds` on. Every thread of the warp takes part.
+// s: scale of column group 0, the next ones `lds` on. Every thread of the warp takes part; a warp whose
+// row is not to be written does not call it (kFullRow stores all of the row, whatever d says).
 template <int NV, int L>
 MOE_DEV void store_row_e4m3(const float (&v)[NV][8], uint8_t* q, float* s, int64_t lds, int d, int th, int t) {
     uint32_t m[2 * NV];

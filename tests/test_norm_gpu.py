@@ -318,3 +318,36 @@ def test_tensors_that_do_not_fit_are_refused():
         b.norm_backward(p, x, y, torch.empty(T, device="cuda"), torch.empty(T, device="cuda"), torch.empty_like(x),
                         torch.zeros(256, dtype=torch.uint8, device="cuda"), dw=torch.empty(d, device="cuda"),
                         weight=torch.ones(d, device="cuda"))
+
+
+# Many rows of 8 bits: copied ahead, several rows a block, the last block of rows not full (rows a block:
+# 8, 4, 2 or 1 by d). 256 to 4096 are whole numbers of the layout's groups, the others end inside one.
+@pytest.mark.parametrize("T,d", [(1201, 256), (1185, 512), (1203, 512), (593, 1024), (1001, 1024), (301, 2048), (613, 2048),
+                                 (303, 4096), (4095, 256), (1201, 240), (613, 2032), (303, 4080), (151, 8192)])
+@pytest.mark.parametrize("stream,kind", [("f32", "rms"), ("bf16", "layer"), ("f16", "rms")])
+def test_many_rows_in_8_bits(T, d, stream, kind):
+    rng = np.random.default_rng([T, d, 4])
+    sc, st = DT[stream]
+    x = make(rng, (T, d), st, 2.0)
+    w, bias, gate = make(rng, (d,), torch.float32, 0.3, 1.0), make(rng, (d,), torch.float32), make(rng, (T,), torch.float32)
+
+    def rows8():
+        return (torch.full((T, d), 77, dtype=torch.uint8, device="cuda"), torch.full(((d + 127) // 128, T), -5.0, device="cuda"))
+
+    def same(q, s, y, what):
+        rq, rs = o.quantize_rows(y.cpu().numpy())
+        gs, gq = s.cpu().numpy(), o.e4m3_values(q.cpu().numpy())
+        assert np.array_equal(gs[:, 0], rs[:, 0]) and np.array_equal(gq[0], rq[0]), f"{what}: row 0"
+        assert np.array_equal(gs, rs) and np.array_equal(gq, rq), what
+    p = b.norm_params(T, d, KIND[kind], eps=EPS, stream_dtype=sc, block_dtype=b.DT_F32)
+    y, (q, s) = torch.empty(T, d, device="cuda"), rows8()
+    b.norm_forward(p, x, y, weight=w, bias=bias, q8=q, s8=s)
+    same(q, s, y, "before the block")
+    q2, s2 = rows8()
+    b.norm_forward(p, x, None, weight=w, bias=bias, q8=q2, s8=s2)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    pj = b.norm_params(T, d, KIND[kind], KIND[kind], eps=EPS, stream_dtype=sc, block_dtype=b.DT_F32, gate_kind=b.GATE_TOKEN,
+                       alpha=0.75, beta=-1.5)
+    out, xn, (q, s) = torch.empty(T, d, dtype=st, device="cuda"), torch.empty(T, d, device="cuda"), rows8()
+    b.norm_residual_forward(pj, x, y, out, weight=w, bias=bias, gate=gate, next_weight=w, next_bias=bias, x_next=xn, q8=q, s8=s)
+    same(q, s, xn, "after the block")
