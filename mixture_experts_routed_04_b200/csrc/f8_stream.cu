@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4) f8_stream_kernel(cons
             uint32_t m = keep ? abs_bits(v) : 0u;
 #pragma unroll
             for (int o = 1; o < kCols; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            if (c == 0) amax[strip][r] = m;
+            if (mine && c == 0) amax[strip][r] = m;  // one strip: half of the threads have none
             cluster_sync_all();
 #pragma unroll
             for (int k = 0; k < S; ++k) {

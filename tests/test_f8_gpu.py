@@ -450,3 +450,12 @@ def test_tiles_with_tiny_wait_limit_report_and_recover(out):
     assert err & ~b.DEVERR_TIMEOUT == 0, f"unexpected error bits {err:#x}"
     check_gated((R, K, N, E, 0), 0.0, out, "tensor")
     check_matmul(R, K, N, E, 0, "f32", "tensor", False)
+
+
+# One token's rows to e4m3: one strip of columns a block up to ceil(N / 128) * 8 * chunks of 3 blocks an SM, above it
+# two; the chunks are the rows by 8, or as many as the rows may make of the experts.
+@pytest.mark.parametrize("shape", [(1, 512, 128, 1, 0), (1, 4096, 1536, 1, 0), (8, 1040, 144, 1, 0), (17, 256, 1536, 1, 0),
+                                   (8, 2048, 128, 8, 0), (8, 512, 768, 8, 0), (8, 512, 1536, 8, 0), (8, 128, 272, 256, 0),
+                                   (70, 384, 1536, 1, 0)], ids=str)
+def test_gated_strips(shape):
+    check_gated(shape, 7.0, "e4m3", "stream")
