@@ -40,13 +40,14 @@ MOE_DEV float max_nan(float a, float b) {
 
 // silu(clamp(g)) clamp(u); L: the limit, infinity without one. The exponential and the
 // reciprocal are the hardware's approximate ones: relative error about 1e-6 (as in the bf16
-// kernels), far below the rounding of the results to 16 or 8 bits.
+// kernels), far below the rounding of the results to 16 or 8 bits. silu(g) first: g u alone may pass
+// the largest fp32 value where the result does not (g = -50, u = 1e38).
 MOE_DEV float gated(float g, float u, float L) {
     g = max_nan(min_nan(g, L), -L);
     u = max_nan(min_nan(u, L), -L);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));
-    return g * u * r;
+    return g * r * u;
 }
 
 // The gate weight of a row (1 without).

@@ -459,3 +459,30 @@ def test_tiles_with_tiny_wait_limit_report_and_recover(out):
                                    (70, 384, 1536, 1, 0)], ids=str)
 def test_gated_strips(shape):
     check_gated(shape, 7.0, "e4m3", "stream")
+
+
+@pytest.mark.parametrize("variant", ["tensor", "stream"])
+@pytest.mark.parametrize("out", ["f32", "e4m3"])
+def test_gated_of_large_projections(variant, out):
+    """Without a limit, h = silu(g) u where g u alone would pass fp32's largest value: one row with a single 1, column n's
+    g and u are its block's scales. At g = -80 the exponential's argument in powers of two, 116, rounds by 2^-18, which
+    moves h by ln 2 of that; three roundings and the reciprocal stay below the rest of 2^-18. e4m3: half a step more."""
+    gu = [(-50.0, 1e38), (-1e20, 1e20), (-80.0, -3e37), (30.0, 1e37), (1e-20, 1e38), (-1e38, 1e-38)]
+    R, K, N = 3, 16, 128 * len(gu)
+    a = torch.zeros(R, K, dtype=torch.uint8, device="cuda")
+    a[1, 5] = 0x38  # 1.0
+    w = torch.full((1, N, K), 0x38, dtype=torch.uint8, device="cuda")
+    sa = torch.ones(1, R, device="cuda")
+    sg, su = (torch.tensor([v[i] for v in gu], device="cuda").view(1, -1, 1).contiguous() for i in (0, 1))
+    p = b.f8_params(R, K, N, out_dtype=b.DT_E4M3 if out == "e4m3" else b.DT_F32, variant=VARIANTS[variant])
+    h = torch.empty(R, N, dtype=torch.uint8 if out == "e4m3" else torch.float32, device="cuda")
+    hs = torch.empty(len(gu), R, device="cuda") if out == "e4m3" else None
+    b.gated_f8(p, a, sa, w, sg, w, su, h, b.f8_workspace(p), h_scale=hs)
+    got = values(h, hs) if out == "e4m3" else h.double().cpu().numpy()
+    g, u = (np.repeat(s.double().cpu().numpy().reshape(-1), 128) for s in (sg, su))
+    ref = np.zeros((R, N))
+    with np.errstate(under="ignore"):
+        ref[1] = o.gated(g, u, 0.0)
+    assert np.isfinite(got).all()
+    tol = (2.0 ** -18 + (2.0 ** -4 if out == "e4m3" else 0.0)) * np.abs(ref) + 2.0 ** -126
+    assert (np.abs(got - ref) <= tol).all()
