@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256, DT == MOE_DT_F32 ? 3 : 4) quantize_rows_k
     float(*mine)[33] = held[threadIdx.x >> 5];
     const int n = n_rows ? min(rows, max(0, *n_rows)) : rows;
     const bool wide = (reinterpret_cast<uintptr_t>(s) & 15) == 0 && rows % 4 == 0;
-    const int units = (n + RPW - 1) / RPW, warps = gridDim.x * (blockDim.x >> 5);
+    const int units = int((uint32_t(n) + RPW - 1) / RPW), warps = gridDim.x * (blockDim.x >> 5);
     const int first = RPW > 1 ? 0 : int(blockIdx.y) * kChunk, last = RPW > 1 ? K : min(K, first + kChunk);
     bool bad = false;
     for (int64_t u = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < units; u += warps) {

@@ -486,3 +486,32 @@ def test_gated_of_large_projections(variant, out):
     assert np.isfinite(got).all()
     tol = (2.0 ** -18 + (2.0 ** -4 if out == "e4m3" else 0.0)) * np.abs(ref) + 2.0 ** -126
     assert (np.abs(got - ref) <= tol).all()
+
+
+ROWS_MOST = 2 ** 31 - 1
+needs_room = pytest.mark.skipif(torch.cuda.is_available() and torch.cuda.mem_get_info()[0] < 120 << 30,
+                                reason="2^31 - 1 rows take 90 GB")
+
+
+def periodic(table, got):
+    """Row r of got is table's row r % 5: compared 5 * 2^24 rows at a time."""
+    step = 5 << 24
+    want = table.repeat(1 << 24, 1)
+    for r in range(0, got.shape[0], step):
+        part = got[r:r + step]
+        if not torch.equal(part, want[:part.shape[0]]):
+            return False
+    return True
+
+
+@needs_room
+def test_most_rows_rounded():
+    x = torch.randn(5, 16, device="cuda").bfloat16()
+    q, s = torch.zeros(ROWS_MOST, 16, dtype=torch.uint8, device="cuda"), torch.zeros(1, ROWS_MOST, device="cuda")
+    idx = torch.arange(ROWS_MOST, dtype=torch.int32, device="cuda").remainder_(5)
+    b.quantize_f8(x, q, s, ws256(), row_index=idx)
+    one, so = torch.empty(5, 16, dtype=torch.uint8, device="cuda"), torch.empty(1, 5, device="cuda")
+    b.quantize_f8(x, one, so, ws256())
+    assert periodic(one, q) and periodic(so.t(), s.t())
+    del q, s, idx
+    torch.cuda.empty_cache()
