@@ -80,7 +80,7 @@ MOE_DEV void count_chunks(const Args& p, int chunk, Chunks& c) {
         c.off[t] = off;
         if (t == p.E - 1) c.off[t + 1] = end;
         if (off < 0 || end < off || end > p.rows) set_error(p.err, MOE_DEVERR_BOUNDS);
-        else cnt = (end - off + chunk - 1) / chunk;
+        else cnt = int((uint32_t(end - off) + chunk - 1) / chunk);
     }
     int s = cnt;
 #pragma unroll

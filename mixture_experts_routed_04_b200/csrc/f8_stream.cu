@@ -67,7 +67,7 @@ MOE_DEV bool find_rows(const Args& p, int u, int chunk, int* sm, int& e, int64_t
             cnt = 0;
         }
     }
-    const int c = (cnt + chunk - 1) / chunk;
+    const int c = int((uint32_t(cnt) + chunk - 1) / chunk);
     int s = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -515,3 +515,22 @@ def test_most_rows_rounded():
     assert periodic(one, q) and periodic(so.t(), s.t())
     del q, s, idx
     torch.cuda.empty_cache()
+
+
+@needs_room
+@pytest.mark.parametrize("variant", ["tensor", "stream"])
+def test_most_rows_multiplied(variant):
+    rng = np.random.default_rng(6)
+    one, so = rows8(rng, 5, 16)
+    w, sw = weights8(rng, 1, 8, 16)
+    ref = torch.empty(5, 8, dtype=torch.bfloat16, device="cuda")
+    b.matmul_f8(b.f8_params(5, 16, 8, variant=VARIANTS[variant]), one, so, w, sw, ref, ws256())
+    a = one.repeat((ROWS_MOST + 4) // 5, 1)[:ROWS_MOST]
+    sa = so.repeat(1, (ROWS_MOST + 4) // 5)[:, :ROWS_MOST].contiguous()
+    c = torch.zeros(ROWS_MOST, 8, dtype=torch.bfloat16, device="cuda")
+    p = b.f8_params(ROWS_MOST, 16, 8, variant=VARIANTS[variant])
+    ws = b.f8_workspace(p)
+    b.matmul_f8(p, a, sa, w, sw, c, ws, offsets=torch.tensor([0, ROWS_MOST], dtype=torch.int32, device="cuda"))
+    assert b.get_error(ws) == 0 and periodic(ref, c)
+    del a, sa, c
+    torch.cuda.empty_cache()
