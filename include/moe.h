@@ -668,6 +668,17 @@ MOE_API int moe_gated_f8(const moe_f8_params* p, const uint8_t* a, const float* 
               float* h_scale, void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
+ * Self-test of the 8-bit tiles' failure path, as moe_wait_selftest for the wait alone: a small product (gated != 0:
+ * moe_gated_f8 with e4m3 results, else moe_matmul_f8) of tensors inside ws, whose copies stop after `blocks`
+ * (0 .. 7) of its 8 blocks along K. The waits for the rest give up after limit_ns (1 .. 1e10; the clock is read
+ * every 64 polls, 0.3 ms), MOE_DEVERR_TIMEOUT is set in the error word at ws and the kernel returns.
+ * ws: MOE_F8_SELFTEST_BYTES, 256-byte aligned; what lies behind its first 256 bytes is overwritten or left.
+ */
+#define MOE_F8_SELFTEST_BYTES (1 << 20)
+MOE_API int moe_f8_wait_selftest(int32_t gated, int32_t blocks, uint64_t limit_ns, void* ws, size_t ws_bytes,
+              moe_stream_t stream);
+
+/*
  * Number of kernel launches one call of `which` (MOE_WS_ROUTE .. MOE_WS_BACKWARD,
  * naming moe_route .. moe_forward_host, moe_route_stats, moe_expert_ffn_backward)
  * makes with these params, into *n (host). For moe_expert_ffn_backward the count

@@ -32,6 +32,7 @@ DT_F32, DT_BF16, DT_F16, DT_E4M3 = range(4)
 NORM_NONE, NORM_RMS, NORM_LAYER = range(3)
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN = range(3)
 NORM_MAX_D = 8192  # MOE_NORM_MAX_D
+F8_SELFTEST_BYTES = 1 << 20  # MOE_F8_SELFTEST_BYTES
 WS_ROUTE, WS_PERMUTE, WS_EXPERT_FFN, WS_COMBINE, WS_FORWARD, WS_FORWARD_HOST, WS_ROUTE_STATS, WS_BACKWARD = range(8)
 
 # every entry point declared in include/moe.h
@@ -43,7 +44,7 @@ EXPORTS = ("moe_version", "moe_status_string", "moe_capacity", "moe_max_rows", "
            "moe_route_stats", "moe_expert_ffn_backward", "moe_variant_table",
            "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward", "moe_norm_residual_forward",
            "moe_norm_residual_backward", "moe_quantize_f8", "moe_quantize_f8_weights", "moe_f8_workspace_size",
-           "moe_matmul_f8", "moe_gated_f8")
+           "moe_matmul_f8", "moe_gated_f8", "moe_f8_wait_selftest")
 NOALLOC_MAX_PAIRS = 262144  # MOE_NOALLOC_MAX_PAIRS
 
 # kernel ids (MOE_K_*), in order
@@ -144,6 +145,7 @@ def lib() -> ctypes.CDLL:
             "moe_f8_workspace_size": ([F], _S),
             "moe_matmul_f8": ([F] + [_V] * 9 + [_S, _V], ctypes.c_int),
             "moe_gated_f8": ([F] + [_V] * 10 + [_S, _V], ctypes.c_int),
+            "moe_f8_wait_selftest": ([i32, i32, ctypes.c_uint64, _V, _S, _V], ctypes.c_int),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -582,3 +584,9 @@ def gated_f8(p: F8Params, a, a_scale, w_gate, s_gate, w_up, s_up, h, ws, h_scale
           ("h_scale", h_scale, ((p.N + 127) // 128, p.rows), _dtypes(DT_F32), True))
     check(lib().moe_gated_f8(ctypes.byref(p), _p(a), _p(a_scale), _p(offsets), _p(w_gate), _p(s_gate), _p(w_up),
                              _p(s_up), _p(h), _p(h_scale), _p(ws), ws.numel(), _stream(stream)), "moe_gated_f8")
+
+
+def f8_wait_selftest(gated, blocks, limit_ns, ws, stream=None):
+    """moe_f8_wait_selftest: an 8-bit product whose copies stop after `blocks` blocks along K; sets DEVERR_TIMEOUT."""
+    check(lib().moe_f8_wait_selftest(int(bool(gated)), int(blocks), int(limit_ns), _p(ws), ws.numel(), _stream(stream)),
+          "moe_f8_wait_selftest")

@@ -60,6 +60,7 @@ Args args_of(const moe_f8_params* p, const uint8_t* a, const float* a_scale, con
     x.limit = p->swiglu_limit > 0.f ? p->swiglu_limit : std::numeric_limits<float>::infinity();
     x.err = static_cast<uint32_t*>(ws);
     x.wait_ns = wait_limit_ns();
+    x.copies = -1;
     return x;
 }
 
@@ -133,6 +134,39 @@ int moe_gated_f8(const moe_f8_params* p, const uint8_t* a, const float* a_scale,
     x.b_scale[1] = s_up;
     x.h_scale = h_scale;
     return f8::launch(p, x, true, stream);
+}
+
+int moe_f8_wait_selftest(int32_t gated, int32_t blocks, uint64_t limit_ns, void* ws, size_t ws_bytes,
+                         moe_stream_t stream) {
+    // three M-tiles and two n-tiles, the last M-tile partial, 8 blocks along K, all in the workspace
+    constexpr int R = 300, K = 1024, N = 256, KB = K / 128, NB = N / 128;
+    if (!ws || blocks < 0 || blocks >= KB || limit_ns == 0 || limit_ns > 10000000000ull) return MOE_ERR_INVALID_ARG;
+    if (!f8::al(ws, 256)) return MOE_ERR_MISALIGNED;
+    if (ws_bytes < MOE_F8_SELFTEST_BYTES) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    uint8_t* at = static_cast<uint8_t*>(ws) + 256;
+    auto take = [&](size_t n) {
+        uint8_t* r = at;
+        at += (n + 255) & ~size_t(255);
+        return r;
+    };
+    const uint8_t* a = take(size_t(R) * K);
+    const uint8_t* b = take(size_t(N) * K);
+    const float* a_scale = reinterpret_cast<float*>(take(size_t(KB) * R * 4));
+    const float* b_scale = reinterpret_cast<float*>(take(size_t(NB) * KB * 4));
+    float* h_scale = reinterpret_cast<float*>(take(size_t(NB) * R * 4));
+    void* out = take(size_t(R) * N * 4);
+    static_assert(256 + R * K + N * K + KB * R * 4 + NB * KB * 4 + NB * R * 4 + R * N * 4 + 6 * 255 <= MOE_F8_SELFTEST_BYTES,
+                  "the workspace holds every tensor");
+    moe_f8_params p{};
+    p.rows = R; p.K = K; p.N = N; p.E = 1;
+    p.out_dtype = gated ? MOE_DT_E4M3 : MOE_DT_F32;
+    f8::Args x = f8::args_of(&p, a, a_scale, nullptr, out, ws);
+    x.b[0] = x.b[1] = b;
+    x.b_scale[0] = x.b_scale[1] = b_scale;
+    x.h_scale = gated ? h_scale : nullptr;
+    x.wait_ns = limit_ns;
+    x.copies = blocks;
+    return f8::launch_tile(x, gated != 0, stream) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

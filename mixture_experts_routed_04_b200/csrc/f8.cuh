@@ -24,6 +24,7 @@ struct Args {
     float limit;              // of the gated form; infinity: none
     uint32_t* err;
     uint64_t wait_ns;
+    int copies;               // tiles: blocks along K a CTA's producer brings; -1: all (else moe_f8_wait_selftest)
 };
 
 // min and max that keep a NaN

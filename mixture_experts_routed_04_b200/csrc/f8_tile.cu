@@ -222,13 +222,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (one thread)
             if (lane == 0) {
-                int stage = 0;
+                int stage = 0, left = p.copies;
                 uint32_t phase = 0, issued = 0, issued_par = 0;
                 bool ok = true;
                 for (int u = blockIdx.x; ok && u < total; u += gridDim.x) {
                     const Unit U = unit_of(u, nt, p, ms);
                     for (int kb = 0; kb < p.KB; ++kb) {
-                        if (!wait(ms->empty + stage, phase ^ 1u)) {
+                        if (left-- == 0 || !wait(ms->empty + stage, phase ^ 1u)) {
                             ok = false;
                             break;
                         }

@@ -127,3 +127,10 @@ def test_f8_buffers(lib):
     assert weights(E=0) == INVALID and weights(N=12) == INVALID and weights(K=24) == INVALID and weights(t=2) == INVALID
     assert weights(N=(1 << 31) - 8) == INVALID
     assert weights(w=None) == INVALID and weights(q=odd) == MISALIGNED and weights(dt=3) == INVALID
+
+
+def test_f8_selftest_arguments(lib):
+    def run(gated=0, blocks=3, limit=1000, ws=P, n=b.F8_SELFTEST_BYTES):
+        return lib.moe_f8_wait_selftest(gated, blocks, limit, ws, n, None)
+    assert run(blocks=-1) == INVALID and run(blocks=8) == INVALID and run(limit=0) == INVALID and run(limit=10 ** 11) == INVALID
+    assert run(ws=None) == INVALID and run(ws=ctypes.c_void_p(4112)) == MISALIGNED and run(n=1 << 19) == TOO_SMALL

@@ -534,3 +534,18 @@ def test_most_rows_multiplied(variant):
     assert b.get_error(ws) == 0 and periodic(ref, c)
     del a, sa, c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("blocks", [0, 1, 3, 5, 7])
+def test_tiles_whose_copies_stop_report_it(blocks, gated):
+    """No wait of a product that runs as it should lasts the 64 polls between two looks at the clock (0.3 ms), so that a
+    short limit alone makes none run out. Here the copies stop: every CTA's waits run out, and the next calls are right."""
+    ws = torch.zeros(b.F8_SELFTEST_BYTES, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        b.f8_wait_selftest(gated, blocks, 1_000_000, ws)  # 1 ms
+        assert b.get_error(ws) == b.DEVERR_TIMEOUT
+        b.clear_error(ws)
+        assert b.get_error(ws) == 0
+    check_gated((300, 1024, 256, 1, 0), 7.0, "e4m3", "tensor")
+    check_matmul(300, 1024, 256, 1, 0, "f32", "tensor", False)
