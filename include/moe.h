@@ -599,8 +599,8 @@ MOE_API int moe_norm_residual_backward(const moe_norm_params* p, const void* y, 
  * for each block of 128: of a row's columns (activations), or of 128 x 128 (weights).
  *   rows     q [rows, K] bytes; scales [ceil(K/128), rows]: x[r, c] = q[r, c] * s[c / 128, r]
  *   weights  q [E, N, K] bytes, K-major; scales [E, ceil(N/128), ceil(K/128)]
- *   s = max(amax / 448, 2^-126), q = e4m3(x / s), nearest even; an infinity or a NaN makes its
- *   whole block read back as NaN.
+ *   s = max(amax / 448, 2^-126), q = e4m3(x / s), nearest even, both quotients rounded to fp32; an
+ *   infinity or a NaN makes its whole block read back as NaN.
  * K is a multiple of 16 up to MOE_F8_MAX_K, N of 8 with E * N <= 2^31 - 256; the last block of either may be
  * partial. Byte tensors lie on 16 bytes (MOE_ERR_MISALIGNED). Rows by expert are as moe_permute leaves them: expert e has rows
  * [offsets[e], offsets[e+1]); rows from offsets[E] on have no part in any result and are not written.
@@ -648,7 +648,8 @@ MOE_API size_t moe_f8_workspace_size(const moe_f8_params* p);
  * and added in fp32.
  * a, a_scale  [rows, K] bytes, [ceil(K/128), rows]; b, b_scale: weights as above
  * offsets     int32 [E+1], or NULL with E = 1 (every row)
- * sorted_pair, topk_w  w_r = topk_w[sorted_pair[r]] (1 where sorted_pair[r] < 0), as moe_expert_ffn
+ * sorted_pair, topk_w  w_r = topk_w[sorted_pair[r]] (1 where sorted_pair[r] < 0; not checked against
+ *             topk_w's length), as moe_expert_ffn
  *             weighs its rows for moe_combine (out_dtype MOE_DT_F16); both NULL: 1
  * out         [rows, N] out_dtype; MOE_DT_F16 values beyond +-65504 set MOE_DEVERR_RANGE
  */

@@ -40,9 +40,10 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// How a row gets into registers: element by element (any alignment), by 16-byte loads (few rows,
-// where the way is shortest), or by 16-byte asynchronous copies of the next rows into shared memory
-// (many rows: HBM stays busy while a row is summed). kStagedFull: rows of exactly 8 * NV * 32 W.
+// How a row gets into registers: element by element (any alignment), by loads of 4 elements (8 bytes of
+// 16 bits, 16 of fp32: few rows, where the way is shortest, and any number of rows that lie on 4 elements'
+// bytes but not on 16), or by 16-byte asynchronous copies of the next rows into shared memory (many rows:
+// HBM stays busy while a row is summed). kStagedFull: rows of exactly 8 * NV * 32 W.
 enum Mode { kScalar = 0, kVec = 1, kStaged = 2, kStagedFull = 3 };
 __host__ __device__ constexpr int layout_of(int mode) { return mode == kScalar ? kScalarRow : mode == kStagedFull ? kFullRow : kVecRow; }
 
@@ -285,7 +286,9 @@ struct NormBwdArgs {
 // Backward blocks an SM (their registers): also the grid, whose partial sums are written and read once
 // more, so few enough that they stay small beside the rows. In vectors the copies ahead keep HBM busy
 // (4096 rows of 2048 bf16: 18.2 us with 2 blocks and 96 registers, 21.2 with 3, 27.5 with 4, whose
-// registers do not hold a row); element by element the warps do (rows of 2047: 67.8, 56.0, 47.9 us).
+// registers do not hold a row); element by element the warps do (rows of 2047: 67.8, 56.0, 47.9 us, although
+// the 64 registers that four blocks leave a thread spill 300 to 1300 bytes). Rows of more than 4096 (NV of 4)
+// spill up to 1200 bytes at 128 registers too: 2048 rows of 8192 bf16 60 us, 2.2 TB/s.
 __host__ __device__ constexpr int bwd_blocks(int nv, int mode) { return mode == kScalar && nv <= 2 ? 4 : 2; }
 constexpr int kBwdBlocksMost = 4;
 
